@@ -78,6 +78,7 @@ typedef enum fos_round {
 /* bits OR-ed into *status by the device */
 #define FOS_STATUS_NONFINITE 0x1u /* a NaN or Inf was read; outputs unspecified */
 #define FOS_STATUS_TIMEOUT 0x2u   /* a bounded device-side wait gave up */
+#define FOS_STATUS_INDEX 0x4u     /* a slot, position, page or length read on the device is out of range */
 
 typedef struct fos_options {
   int32_t fmt;         /* fos_format */
@@ -317,6 +318,127 @@ fos_status fos_quantize_static(const void* x, int64_t batch, int64_t rows, int64
                                int64_t ld, const fos_options* opt, const float* amax_in,
                                const fos_qtensor* rowwise, const fos_qtensor* colwise,
                                uint32_t* status, void* stream);
+
+/*
+ * The key/value cache: keys and values of attention held in NVFP4, in pages.
+ *
+ * A pool holds num_pages pages of page_size tokens (16, 32, 64 or 128) for
+ * `heads` key/value heads of head_dim values (64 or 128).  Keys and values
+ * are separate pools with the same strides:
+ *   codes  [num_pages][heads][page_size][head_dim / 2]   packed E2M1
+ *   scales [num_pages][heads][page_size][head_dim / 16]  E4M3, one for each
+ *          16 consecutive values of a token's head
+ * A page is contiguous; pages are codes_page_stride and scales_page_stride
+ * bytes apart (>= the page's size, multiples of 16), so one allocation may
+ * hold the pools of several layers.  All pointers 16-byte aligned.
+ *   k_tensor_scale, v_tensor_scale: float [heads], the FP32 scale S_t of each
+ *          head, fixed before the first token is appended: A / (4 * 448) for
+ *          4/6, A / (6 * 448) for 6-only, A the largest |value| expected.
+ *          Larger values saturate, as with a supplied amax in fos_quantize.
+ * A slot is page * page_size + position in the page.
+ */
+typedef struct fos_kv_cache {
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const float* k_tensor_scale;
+  const float* v_tensor_scale;
+  int64_t num_pages;
+  int64_t page_size;
+  int64_t heads;
+  int64_t head_dim;
+  int64_t codes_page_stride;
+  int64_t scales_page_stride;
+} fos_kv_cache;
+
+/* The position rotation: the first `dim` values of every head turned in
+ * pairs by the angles of a table float [max_positions][dim], each row dim/2
+ * cosines and then dim/2 sines.  Pair i is (x[i], x[i + dim/2]), or
+ * (x[2i], x[2i + 1]) when interleaved.  dim: a multiple of 16, <= head_dim;
+ * table 16-byte aligned. */
+typedef struct fos_rotary {
+  const float* table;
+  const int32_t* positions; /* [tokens] */
+  int64_t max_positions;
+  int32_t dim;
+  int32_t interleaved;
+} fos_rotary;
+
+/*
+ * fos_kv_append -- quantize the keys and values of `tokens` tokens into the
+ * cache, rotating the keys (and queries) on the way.
+ *   k, v   bf16 [tokens][heads][head_dim], tokens k_ld / v_ld elements apart
+ *          (>= heads * head_dim, multiples of 8), 16-byte aligned.
+ *   slots  int64 [tokens]; a negative slot skips its token (padding).  Slots
+ *          are distinct: what a slot that occurs twice then holds is
+ *          unspecified.  A slot >= num_pages * page_size is skipped and sets
+ *          FOS_STATUS_INDEX.
+ *   rot    NULL for no rotation.  A pair (a, b) at angle (c, s) becomes
+ *          a' = bf16(RN(a c) - RN(b s)), b' = bf16(RN(b c) + RN(a s)), in
+ *          binary32 with those roundings.  A position outside [0,
+ *          max_positions) sets FOS_STATUS_INDEX and skips the token (its
+ *          q_out row too).
+ *   q, q_out  bf16 [tokens][q_heads][head_dim] with strides q_ld, q_out_ld;
+ *          NULL to rotate keys only.  q_out may be q.  Needs rot.  Queries of
+ *          skipped slots are rotated too.
+ * The 16-value blocks of the rotated keys and of the values are quantized by
+ * fos_quantize's rule (fmt NVFP4_46 or NVFP4_6, 1x16, RNE) with S_t of their
+ * head: the same codes and scales, bit for bit.  NaN/Inf in a token that is
+ * written sets FOS_STATUS_NONFINITE; that token's slot is unspecified.
+ */
+fos_status fos_kv_append(const fos_kv_cache* cache, int32_t fmt, const void* k, int64_t k_ld, const void* v,
+                         int64_t v_ld, int64_t tokens, const int64_t* slots, const fos_rotary* rot,
+                         const void* q, int64_t q_ld, void* q_out, int64_t q_out_ld, int64_t q_heads,
+                         uint32_t* status, void* stream);
+
+/*
+ * fos_kv_read -- the keys and values of `tokens` slots as bf16
+ * [tokens][heads][head_dim] (dense, 16-byte aligned), by fos_dequantize's
+ * rule: bf16_rne((q * E4M3(s)) * S_t).  A negative slot reads as zeros; so
+ * does a slot out of range, which sets FOS_STATUS_INDEX.
+ */
+fos_status fos_kv_read(const fos_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
+                       uint32_t* status, void* stream);
+
+/*
+ * fos_kv_attention -- softmax attention of ragged queries over the cache.
+ *   q       bf16 [total_q][q_heads][head_dim], tokens q_ld elements apart
+ *           (a multiple of 8), 16-byte aligned; q_heads a multiple of the
+ *           cache's heads, query head h reads head h / (q_heads / heads).
+ *   cu_q    int32 [batch + 1]: sequence b has the queries cu_q[b] ..
+ *           cu_q[b + 1] - 1.  Queries outside [cu_q[0], cu_q[batch]) are not
+ *           touched: their rows of out and lse stay as they were.
+ *   pages   int32 [batch][max_pages]: the pages of each sequence in order;
+ *           entries that hold no visible token are not read.
+ *   kv_len  int32 [batch]: tokens of each sequence in the cache, those of its
+ *           queries among them when causal.
+ *   max_q   the largest number of queries of a sequence (it chooses between
+ *           kernels; any value gives the same result up to rounding).
+ *   causal  query i of n sees the keys j <= kv_len - n + i, and with window
+ *           > 0 only j > kv_len - n + i - window; otherwise all kv_len keys
+ *           (window must be 0), as over an encoder's states.
+ *   out     bf16 [total_q][q_heads][head_dim], tokens out_ld elements apart.
+ *   lse     float [total_q][q_heads], nullable: log of the sum of
+ *           exp(scale * q.k) over the visible keys.
+ * A query that sees no key gets out = 0 and lse = -inf.  One that sees a key
+ * and holds a NaN or Inf gets NaN.  A visible page outside [0, num_pages), a kv_len
+ * beyond max_pages * page_size or below 0, and a cu_q that descends or
+ * leaves [0, total_q] set FOS_STATUS_INDEX; such keys count as invisible and
+ * such lengths are clamped.
+ *   workspace: fos_kv_attention_workspace_size(...) bytes, 16-byte aligned,
+ *           not initialised, not shared by calls that overlap on the GPU.
+ * Arithmetic: products of queries and cached values are exact, sums are
+ * binary32, the softmax weights are rounded to f16 before the second product.
+ * The work is split by the lengths alone: the same call gives the same bits.
+ */
+size_t fos_kv_attention_workspace_size(const fos_kv_cache* cache, int64_t total_q, int64_t batch, int64_t q_heads,
+                                       int64_t max_q);
+fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_ld, int64_t total_q,
+                            int64_t q_heads, const int32_t* cu_q, int64_t batch, const int32_t* pages,
+                            int64_t max_pages, const int32_t* kv_len, int64_t max_q, float scale, int32_t causal,
+                            int64_t window, void* out, int64_t out_ld, float* lse, void* workspace,
+                            size_t workspace_bytes, uint32_t* status, void* stream);
 
 /* Bytes of workspace fos_quantize needs for this call. */
 size_t fos_workspace_size(int64_t batch, int64_t rows, int64_t cols, const fos_options* opt);

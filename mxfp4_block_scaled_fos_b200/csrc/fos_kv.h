@@ -1,0 +1,63 @@
+// fos_kv.h -- launch descriptors of the key/value cache's kernels (host
+// side; no device code).  Semantics: include/fos.h.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fos.h"
+
+namespace fos {
+
+// The pools of one cache; strides in bytes.
+struct KvPool {
+  uint8_t *kc, *ks, *vc, *vs;
+  const float *kst, *vst;
+  long long codes_stride, scales_stride;  // between pages
+  long long num_pages;
+  int page_shift;                         // log2(page_size)
+  int heads, dim;
+};
+
+struct KvAppendArgs {
+  KvPool p;
+  const uint16_t *k, *v, *q;              // q nullable
+  uint16_t* q_out;
+  long long k_ld, v_ld, q_ld, q_out_ld;
+  const int64_t* slots;
+  const float* table;                     // nullable: no rotation
+  const int32_t* positions;
+  long long max_positions;
+  int rot, tokens, q_heads;
+  uint32_t* status;
+  float neg_zero = -0.0f;                 // opaque -0 (see QuantArgs)
+};
+
+struct KvReadArgs {
+  KvPool p;
+  const int64_t* slots;
+  int tokens;
+  uint16_t *k, *v;
+  uint32_t* status;
+};
+
+struct KvAttnArgs {
+  KvPool p;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;                             // nullable
+  long long q_ld, out_ld;
+  const int32_t *cu_q, *pages, *kv_len;
+  long long max_pages;
+  int total_q, batch, q_heads, group;     // group = q_heads / heads
+  int causal;
+  long long window;                       // 0: none
+  float scale_log2;                       // scale * log2(e)
+  uint32_t* status;
+};
+
+cudaError_t launch_kv_append(const KvAppendArgs& a, int fmt, bool interleaved, cudaStream_t st);
+cudaError_t launch_kv_read(const KvReadArgs& a, cudaStream_t st);
+cudaError_t launch_kv_attention(const KvAttnArgs& a, cudaStream_t st);
+
+}  // namespace fos

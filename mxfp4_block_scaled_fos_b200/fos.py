@@ -28,6 +28,7 @@ FLAG_SCALE_SWIZZLED = 0x2
 FLAG_RHT16_COL = 0x4
 STATUS_NONFINITE = 0x1
 STATUS_TIMEOUT = 0x2
+STATUS_INDEX = 0x4
 
 ERRORS = {
     1: "FOS_ERR_NULL", 2: "FOS_ERR_ALIGN", 3: "FOS_ERR_SHAPE", 4: "FOS_ERR_UNSUPPORTED",
@@ -38,7 +39,8 @@ ERRORS = {
 EXPORTS = ("fos_quantize", "fos_quantize_host", "fos_amax", "fos_dequantize", "fos_workspace_size",
            "fos_scales_size", "fos_status_string", "fos_version", "fos_quantize_static",
            "fos_testing_quantize_stalled", "fos_testing_quantize_2d_strip", "fos_fake_quantize",
-           "fos_gemm_nvfp4", "fos_gemm_nvfp4_ws", "fos_gemm_workspace_size")
+           "fos_gemm_nvfp4", "fos_gemm_nvfp4_ws", "fos_gemm_workspace_size", "fos_kv_append", "fos_kv_read",
+           "fos_kv_attention", "fos_kv_attention_workspace_size")
 
 
 class Options(ctypes.Structure):

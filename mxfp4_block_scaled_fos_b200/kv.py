@@ -1,0 +1,287 @@
+"""The key/value cache in NVFP4: keys and values of attention held as packed
+E2M1 codes with Four Over Six block scales, in pages.
+
+    cache = fos.KVCache.empty(pages, page_size, heads, head_dim, k_amax, v_amax)
+    q = fos.kv_append(cache, k, v, slots, positions=pos, cos_sin=table, q=q)
+    y = fos.kv_attention(cache, q, cu_q, pages, kv_len, max_q)
+
+kv_append rotates the new keys (and queries) to their positions and
+quantizes the keys and values into their slots; kv_attention reads the codes
+and scales; kv_read gives them back as bf16.  This module only checks
+arguments, allocates outputs and workspaces, and hands pointers to the C ABI
+(include/fos.h, where layouts and semantics are).  The calls run on the
+device of their tensors, on `stream` or that device's current stream.
+
+Sources: Ultralytics glossary "FP4", "Como funciona FP4" (NVFP4: 16 values,
+E4M3 block scale, FP32 scale); Hugging Face transformers doc "Four Over
+Six", introduction (the adaptive block scale).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Tuple, Union
+
+import torch
+
+from . import fos
+
+_P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+
+
+class _CacheC(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("k_codes", "k_scales", "v_codes", "v_scales", "k_tensor_scale", "v_tensor_scale")] + \
+        [(n, _I64) for n in ("num_pages", "page_size", "heads", "head_dim", "codes_page_stride",
+                             "scales_page_stride")]
+
+
+class _RotaryC(ctypes.Structure):
+    _fields_ = [("table", _P), ("positions", _P), ("max_positions", _I64), ("dim", _I32), ("interleaved", _I32)]
+
+
+_bound = None
+
+
+def _lib():
+    global _bound
+    if _bound is None:
+        L = fos.lib()
+        CP, RP, sz = ctypes.POINTER(_CacheC), ctypes.POINTER(_RotaryC), ctypes.c_size_t
+        L.fos_kv_append.restype = _I32
+        L.fos_kv_append.argtypes = [CP, _I32, _P, _I64, _P, _I64, _I64, _P, RP, _P, _I64, _P, _I64, _I64, _P, _P]
+        L.fos_kv_read.restype = _I32
+        L.fos_kv_read.argtypes = [CP, _P, _I64, _P, _P, _P, _P]
+        L.fos_kv_attention_workspace_size.restype = sz
+        L.fos_kv_attention_workspace_size.argtypes = [CP, _I64, _I64, _I64, _I64]
+        L.fos_kv_attention.restype = _I32
+        L.fos_kv_attention.argtypes = [CP, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, ctypes.c_float, _I32,
+                                       _I64, _P, _I64, _P, _P, sz, _P, _P]
+        _bound = L
+    return _bound
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+class KVCache:
+    """The pools of one layer: k_codes, v_codes uint8 [pages, heads,
+    page_size, head_dim/2], k_scales, v_scales uint8 [pages, heads,
+    page_size, head_dim/16], k_tensor_scale, v_tensor_scale float32 [heads],
+    all on one device.  Each page is contiguous; the pages of the two codes
+    (and of the two scales) pools are the same distance apart, so slices of a
+    larger allocation work.  fmt: "nvfp4_46" or "nvfp4_6", for what is
+    appended (reading is the same)."""
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+                 k_tensor_scale: torch.Tensor, v_tensor_scale: torch.Tensor, fmt: str = "nvfp4_46"):
+        _need(fmt in ("nvfp4_46", "nvfp4_6"), "fmt must be nvfp4_46 or nvfp4_6")
+        _need(k_codes.dim() == 4, "codes must be [pages, heads, page_size, head_dim/2]")
+        n, h, p, half = k_codes.shape
+        dev = k_codes.device
+        if dev.type != "cuda":
+            raise TypeError("the pools must be CUDA tensors")
+        for t, last in ((k_codes, half), (v_codes, half), (k_scales, half // 8), (v_scales, half // 8)):
+            if t.dtype != torch.uint8:
+                raise TypeError("the pools must be uint8 tensors")
+            _need(tuple(t.shape) == (n, h, p, last) and t.device == dev, "the pools' shapes or devices do not match")
+            _need(t.stride()[1:] == (p * last, last, 1), "a page of a pool must be contiguous")
+        _need(k_codes.stride(0) == v_codes.stride(0) and k_scales.stride(0) == v_scales.stride(0),
+              "the pools of keys and values must have the same distance between pages")
+        for t in (k_tensor_scale, v_tensor_scale):
+            if t.dtype != torch.float32:
+                raise TypeError("the tensor scales must be float32")
+            _need(tuple(t.shape) == (h,) and t.is_contiguous() and t.device == dev,
+                  "the tensor scales must be [heads] on the pools' device")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_tensor_scale, self.v_tensor_scale, self.fmt, self.device = k_tensor_scale, v_tensor_scale, fmt, dev
+        self.pages, self.heads, self.page_size, self.head_dim = n, h, p, 2 * half
+        self._c = _CacheC(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                          k_tensor_scale.data_ptr(), v_tensor_scale.data_ptr(), n, p, h, 2 * half,
+                          k_codes.stride(0), k_scales.stride(0))
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, heads: int, head_dim: int, k_amax: Union[float, torch.Tensor],
+              v_amax: Union[float, torch.Tensor], fmt: str = "nvfp4_46", device="cuda") -> "KVCache":
+        """An uninitialised cache.  k_amax, v_amax: the largest |value| to
+        expect of each head's (rotated) keys and of its values, a number or
+        float32 [heads]; larger ones saturate."""
+        dev = torch.device(device)
+        pools = [torch.empty(pages, heads, page_size, head_dim // n, dtype=torch.uint8, device=dev)
+                 for n in (2, 16, 2, 16)]
+        top = 2688.0 if fmt == "nvfp4_6" else 1792.0
+        # a tensor as divisor: a number would be turned into its reciprocal, which is not the library's rounding
+        top = torch.full((heads,), top, dtype=torch.float32, device=dev)
+        st = [torch.as_tensor(a, dtype=torch.float32, device=dev).expand(heads) / top for a in (k_amax, v_amax)]
+        return cls(*pools, *st, fmt=fmt)
+
+
+class _on:
+    """The tensors' device as the current one, and the stream to use on it."""
+
+    def __init__(self, dev, stream):
+        self._guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        self._dev, self._stream = dev, stream
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        s = self._stream if self._stream is not None else torch.cuda.current_stream(self._dev)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _rows(name: str, x: torch.Tensor, tokens: int, heads: Optional[int], cache: KVCache) -> None:
+    if x.dtype != torch.bfloat16 or x.device != cache.device:
+        raise TypeError("%s must be a bfloat16 tensor on the cache's device" % name)
+    _need(x.dim() == 3 and x.shape[0] == tokens and x.shape[2] == cache.head_dim and
+          (heads is None or x.shape[1] == heads), "%s must be [tokens, heads, head_dim]" % name)
+    _need(x.stride(2) == 1 and x.stride(1) == cache.head_dim, "the heads of a token of %s must be contiguous" % name)
+
+
+def _ints(name: str, x: torch.Tensor, dtype, shape, cache: KVCache) -> None:
+    if x.dtype != dtype or x.device != cache.device:
+        raise TypeError("%s must be a %s tensor on the cache's device" % (name, str(dtype).replace("torch.", "")))
+    _need(tuple(x.shape) == shape and x.is_contiguous(), "%s must be contiguous %s" % (name, list(shape)))
+
+
+def _status(status: Optional[torch.Tensor], cache: KVCache):
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.device != cache.device:
+        raise TypeError("status must be an int32 tensor on the cache's device")
+    return status.data_ptr()
+
+
+def _ld(x: torch.Tensor) -> int:
+    # the distance of a single token is free
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+              positions: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None,
+              interleaved: bool = False, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Quantize k, v bf16 [tokens, heads, head_dim] into the slots (int64
+    [tokens], page * page_size + position in the page; negative: skip).
+
+    cos_sin: float32 [max_positions, dim], dim/2 cosines then dim/2 sines for
+    each position; with it the first dim values of each head of k (and q
+    [tokens, q_heads, head_dim]) are turned by positions (int32 [tokens]), in
+    pairs (i, i + dim/2), or (2i, 2i + 1) when interleaved.  Returns the
+    rotated queries (q_out when given, which may be q), or None without q.
+    fos_kv_append in include/fos.h has the rounding and the errors."""
+    t = k.shape[0]
+    _rows("k", k, t, cache.heads, cache)
+    _rows("v", v, t, cache.heads, cache)
+    _ints("slots", slots, torch.int64, (t,), cache)
+    _need((cos_sin is None) == (positions is None), "positions and cos_sin belong together")
+    rot = None
+    if cos_sin is not None:
+        _ints("positions", positions, torch.int32, (t,), cache)
+        _need(cos_sin.dim() == 2, "cos_sin must be [max_positions, dim]")
+        _ints("cos_sin", cos_sin, torch.float32, tuple(cos_sin.shape), cache)
+        rot = _RotaryC(cos_sin.data_ptr(), positions.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+                       1 if interleaved else 0)
+    if q is not None:
+        _need(rot is not None, "q is rotated: it needs positions and cos_sin")
+        _rows("q", q, t, None, cache)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        else:
+            _rows("q_out", q_out, t, q.shape[1], cache)
+    else:
+        _need(q_out is None, "q_out without q")
+    with _on(cache.device, stream) as s:
+        st = _lib().fos_kv_append(
+            cache._ref, fos.FMT[cache.fmt], k.data_ptr(), _ld(k), v.data_ptr(), _ld(v), t, slots.data_ptr(),
+            None if rot is None else ctypes.byref(rot), None if q is None else q.data_ptr(),
+            0 if q is None else _ld(q), None if q is None else q_out.data_ptr(), 0 if q is None else _ld(q_out),
+            0 if q is None else q.shape[1], _status(status, cache), s)
+    if st != 0:
+        raise fos.FosError(st, "fos_kv_append")
+    return q_out
+
+
+def kv_read(cache: KVCache, slots: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+            status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The keys and values of slots (int64 [tokens]) as the cache holds them:
+    two bf16 tensors [tokens, heads, head_dim], zeros for negative slots."""
+    t = slots.shape[0] if slots.dim() == 1 else -1
+    _ints("slots", slots, torch.int64, (max(t, 0),), cache)
+    if out is None:
+        out = tuple(torch.empty(t, cache.heads, cache.head_dim, dtype=torch.bfloat16, device=cache.device)
+                    for _ in range(2))
+    for x in out:
+        _rows("out", x, t, cache.heads, cache)
+        _need(x.is_contiguous(), "out must be contiguous")
+    with _on(cache.device, stream) as s:
+        st = _lib().fos_kv_read(cache._ref, slots.data_ptr(), t, out[0].data_ptr(), out[1].data_ptr(),
+                                _status(status, cache), s)
+    if st != 0:
+        raise fos.FosError(st, "fos_kv_read")
+    return out[0], out[1]
+
+
+def kv_attention_workspace_size(cache: KVCache, total_q: int, batch: int, q_heads: int, max_q: int) -> int:
+    """Bytes of workspace kv_attention needs."""
+    return int(_lib().fos_kv_attention_workspace_size(cache._ref, total_q, batch, q_heads, max_q))
+
+
+def kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, pages: torch.Tensor, kv_len: torch.Tensor,
+                 max_q: int, causal: bool = True, window: int = 0, scale: Optional[float] = None,
+                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                 workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Attention of ragged queries over the cached keys and values.
+
+    q: bf16 [total_q, q_heads, head_dim], q_heads a multiple of the cache's
+    heads; cu_q int32 [batch + 1], where each sequence's queries begin; pages
+    int32 [batch, max_pages]; kv_len int32 [batch]; max_q the largest number
+    of queries of a sequence.  causal: the queries are the last of their
+    sequence (window > 0: each sees that many keys, its own among them);
+    causal=False: each query sees all keys, as over an encoder's states.
+    scale: 1/sqrt(head_dim) by default.  Returns out bf16, or (out, lse) with
+    return_lse (lse float32 [total_q, q_heads]).  Queries that see no key get
+    zeros and -inf; rows of out and lse that belong to no sequence are left
+    as they were.  fos_kv_attention in include/fos.h has the details."""
+    _rows("q", q, q.shape[0], None, cache)
+    t, hq = q.shape[0], q.shape[1]
+    _need(hq > 0 and hq % cache.heads == 0, "q_heads must be a multiple of the cache's heads")
+    _need(cu_q.dim() == 1 and cu_q.shape[0] >= 1, "cu_q must be [batch + 1]")
+    b = cu_q.shape[0] - 1
+    _ints("cu_q", cu_q, torch.int32, (b + 1,), cache)
+    _need(pages.dim() == 2, "pages must be [batch, max_pages]")
+    _ints("pages", pages, torch.int32, (b, pages.shape[1]), cache)
+    _ints("kv_len", kv_len, torch.int32, (b,), cache)
+    _need(window >= 0 and (causal or window == 0), "window needs causal")
+    if out is None:
+        out = torch.empty(t, hq, cache.head_dim, dtype=torch.bfloat16, device=q.device)
+    else:
+        _rows("out", out, t, hq, cache)
+    if lse is not None:
+        _ints("lse", lse, torch.float32, (t, hq), cache)
+    elif return_lse:
+        lse = torch.empty(t, hq, dtype=torch.float32, device=q.device)
+    with _on(cache.device, stream) as s:
+        L = _lib()
+        need = L.fos_kv_attention_workspace_size(cache._ref, t, b, hq, max_q)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            if stream is not None:
+                workspace.record_stream(stream)
+        elif workspace is not None:
+            _need(workspace.device == cache.device, "workspace must be on the cache's device")
+        st = L.fos_kv_attention(
+            cache._ref, q.data_ptr(), _ld(q), t, hq, cu_q.data_ptr(), b, pages.data_ptr(), pages.shape[1],
+            kv_len.data_ptr(), max_q, 1.0 / math.sqrt(cache.head_dim) if scale is None else scale,
+            1 if causal else 0, window, out.data_ptr(), _ld(out), None if lse is None else lse.data_ptr(),
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _status(status, cache), s)
+    if st != 0:
+        raise fos.FosError(st, "fos_kv_attention")
+    return (out, lse) if return_lse else out

@@ -1,0 +1,410 @@
+"""The key/value cache in 4 bits (mxfp4_block_scaled_fos_b200/kv.py): append
+and read against the oracle bit for bit, attention against a 64-bit
+computation on the same codes with the bound derived in kv_reference.py."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import mxfp4_block_scaled_fos_b200 as F
+import kv_reference as R
+
+from helpers import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+I32 = torch.int32
+
+
+def _table(n, rot):
+    angle = torch.arange(n, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, rot, 2).double() / rot)
+    return torch.cat((angle.cos(), angle.sin()), 1).float()
+
+
+def _random_cache(pages, page, heads, dim, seed, gap=0):
+    """A cache of quantized normal values; `gap` bytes of 16 between its pages."""
+    dev = require_gpu()
+    g = torch.Generator().manual_seed(seed)
+    ref = {}
+    pools = []
+    for name in "kv":
+        x = torch.randn(pages * page, heads, dim, generator=g).to(torch.bfloat16)
+        amax = np.array([5.1 + 0.37 * h for h in range(heads)], np.float32)
+        c, s = R.quantize(x, amax, False)
+        for y, kind in ((c, "c"), (s, "s")):
+            y = np.ascontiguousarray(y.reshape(pages, page, heads, -1).transpose(0, 2, 1, 3))
+            ref[name + kind] = y
+            n = y[0].size
+            whole = torch.full((pages, n + 16 * gap), 0xFF, dtype=torch.uint8, device=dev)
+            t = whole[:, :n].unflatten(1, y.shape[1:])
+            t.copy_(torch.from_numpy(y))
+            pools.append(t)
+        st = torch.from_numpy(amax) / 1792.0
+        ref[name + "st"] = st.numpy()
+        ref[name + "dev"] = st.to(dev)
+    cache = F.KVCache(*pools, ref["kdev"], ref["vdev"])
+    return cache, ref
+
+
+@pytest.mark.parametrize("dim,page,rot,inter,fmt,tokens,heads,q_heads", [
+    (128, 16, 128, False, "nvfp4_46", 1, 1, 1),
+    (128, 16, 128, False, "nvfp4_46", 37, 8, 32),
+    (128, 64, 64, False, "nvfp4_6", 130, 2, 3),
+    (128, 128, 16, True, "nvfp4_46", 5, 3, 24),
+    (64, 16, 64, True, "nvfp4_6", 33, 5, 5),
+    (64, 32, 48, False, "nvfp4_46", 64, 1, 7),
+    (64, 64, 16, False, "nvfp4_46", 1300, 2, 2),
+    (64, 16, 0, False, "nvfp4_46", 50, 4, 0),
+])
+def test_append_and_read_match_the_oracle(dim, page, rot, inter, fmt, tokens, heads, q_heads):
+    dev = require_gpu()
+    g = torch.Generator().manual_seed(tokens + dim)
+    n = -(-tokens // page) + 3
+    k_amax = torch.rand(heads, generator=g) * 3 + 2
+    cache = F.KVCache.empty(n, page, heads, dim, k_amax.to(dev), 2.9, fmt=fmt, device=dev)
+    for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
+        t.fill_(0xA5)
+    # one projection's output: tokens further apart than their heads
+    x = (torch.randn(tokens, q_heads + 2 * heads + 1, dim, generator=g)).to(torch.bfloat16)
+    x[0, -2:, :16] = 0
+    q, k, v = x[:, :q_heads], x[:, q_heads:q_heads + heads], x[:, q_heads + heads:q_heads + 2 * heads]
+    xd = x.to(dev)
+    qd, kd, vd = (xd[:, a:b] for a, b in ((0, q_heads), (q_heads, q_heads + heads),
+                                          (q_heads + heads, q_heads + 2 * heads)))
+    slots = torch.randperm(n * page, generator=g)[:tokens].to(torch.int64)
+    slots[tokens // 2::5] = -1 - slots[tokens // 2::5]
+    status = torch.zeros(1, dtype=I32, device=dev)
+    kw, want_q, want_k = {}, q, k
+    if rot:
+        pos = torch.randint(0, 99, (tokens,), generator=g).to(I32)
+        table = _table(99, rot)
+        want_q, want_k = R.rotate(q, pos, table, inter), R.rotate(k, pos, table, inter)
+        kw = dict(positions=pos.to(dev), cos_sin=table.to(dev), interleaved=inter, q=qd)
+    got_q = F.kv_append(cache, kd, vd, slots.to(dev), status=status, **kw)
+    if rot:
+        assert torch.equal(got_q.cpu().view(torch.int16), want_q.view(torch.int16))
+    else:
+        assert got_q is None
+    assert int(status) == 0
+    live = slots >= 0
+    assert int(live.sum()) == len(set(slots[live].tolist()))
+    out_k, out_v = F.kv_read(cache, slots.to(dev))
+    for want, amax, codes, scales, st, out in (
+            (want_k, k_amax, cache.k_codes, cache.k_scales, cache.k_tensor_scale, out_k),
+            (v, torch.full((heads,), 2.9), cache.v_codes, cache.v_scales, cache.v_tensor_scale, out_v)):
+        c, s = R.quantize(want, amax.numpy(), fmt == "nvfp4_6")
+        for mine, theirs in ((codes, c), (scales, s)):
+            all_rows = np.full((n * page, heads, theirs.shape[-1]), 0xA5, np.uint8)
+            all_rows[slots[live].numpy()] = theirs[live.numpy()]
+            got = mine.transpose(1, 2).reshape(n * page, heads, -1).cpu().numpy()
+            assert np.array_equal(got, all_rows)   # the other slots as they were
+        st = st.cpu().numpy()
+        y = (R.values(c, s).astype(np.float32) * st[:, None]).astype(np.float32)
+        y[~live.numpy()] = 0
+        assert torch.equal(out.cpu(), torch.from_numpy(y).to(torch.bfloat16))
+
+
+def test_append_rotates_queries_in_place_and_reports_bad_indexes():
+    dev = require_gpu()
+    cache = F.KVCache.empty(2, 16, 2, 128, 4.0, 4.0, device=dev)
+    cache.k_codes.fill_(7)
+    x = torch.randn(4, 8, 128, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    xd, table = x.to(dev), _table(10, 128)
+    pos = torch.tensor([3, 10, -1, 9], dtype=I32)     # 10 and -1 are outside the table
+    slots = torch.tensor([5, 6, 7, 32])               # 32 is outside the pool
+    status = torch.zeros(1, dtype=I32, device=dev)
+    q = xd[:, :4]
+    got = F.kv_append(cache, xd[:, 4:6], xd[:, 6:], slots.to(dev), pos.to(dev), table.to(dev), q=q, q_out=q,
+                      status=status)
+    assert got is q and int(status) == F.STATUS_INDEX
+    want = x[:, :4].clone()
+    ok = [0, 3]
+    want[ok] = R.rotate(x[ok, :4], pos[ok], table, False)
+    assert torch.equal(q.cpu().view(torch.int16), want.view(torch.int16))
+    assert torch.equal(xd[:, 4:].cpu(), x[:, 4:])
+    rows = cache.k_codes.transpose(1, 2).reshape(32, -1)
+    assert bool((rows[[i for i in range(32) if i != 5]] == 7).all()) and not bool((rows[5] == 7).all())
+    status.zero_()
+    k, v = F.kv_read(cache, torch.tensor([32, 5, -1], device=dev), status=status)
+    assert int(status) == F.STATUS_INDEX and not k[0].any() and not v[2].any() and bool(k[1].any())
+    status.zero_()
+    bad = xd.clone()
+    bad[1, 6, 77] = math.inf
+    F.kv_append(cache, bad[:, 4:6], bad[:, 6:], torch.arange(4, device=dev), status=status)
+    assert int(status) == F.STATUS_NONFINITE
+
+
+def _check(cache, ref, q, cu, pages, kv_len, causal=True, window=0, scale=None, max_q=None, **kw):
+    dev = require_gpu()
+    scale = 1 / math.sqrt(q.shape[2]) if scale is None else scale
+    out, lse, bound, lbound = R.attention(q, ref["kc"], ref["ks"], ref["vc"], ref["vs"], ref["kst"], ref["vst"],
+                                          cu, pages, kv_len, causal, window, scale)
+    status = torch.zeros(1, dtype=I32, device=dev)
+    n = [b - a for a, b in zip(cu, cu[1:])]
+    got, gl = F.kv_attention(cache, q.to(dev), torch.tensor(cu, dtype=I32, device=dev),
+                             torch.as_tensor(np.asarray(pages), dtype=I32).to(dev),
+                             torch.tensor(kv_len, dtype=I32, device=dev), max(n) if max_q is None else max_q,
+                             causal=causal, window=window, scale=scale, return_lse=True, status=status, **kw)
+    got, gl = got.cpu().double().numpy(), gl.cpu().double().numpy()
+    assert int(status) == 0
+    rows = slice(cu[0], cu[-1])
+    off = np.abs(got - out)[rows] - bound[rows]
+    assert np.isfinite(got[rows]).all() and (off <= 0).all(), (off.max(), np.argwhere(off > 0)[:5])
+    none = np.isinf(lse[rows])
+    assert np.array_equal(np.isneginf(gl[rows]), none)
+    assert (np.abs(gl[rows][~none] - lse[rows][~none]) <= lbound[rows][~none]).all()
+    return got, gl
+
+
+def _paged(kv_len, page, seed, spare=1):
+    """A block table of distinct pages in random order, -1 beyond each length."""
+    need = [-(-m // page) for m in kv_len]
+    order = np.random.RandomState(seed).permutation(sum(need) + spare)
+    table = np.full((len(kv_len), max(1, max(need) + 1)), -1, np.int32)
+    at = 0
+    for b, m in enumerate(need):
+        table[b, :m] = order[at:at + m]
+        at += m
+    return table, sum(need) + spare
+
+
+def _queries(total, heads, dim, seed, gain=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(total, heads, dim, generator=g) * gain).to(torch.bfloat16)
+
+
+# ragged single tokens and drafts: q_heads / heads of 1 to 8, odd lengths, pages that end inside a tile
+@pytest.mark.parametrize("dim,page,heads,group,q_len,kv_len,window", [
+    (128, 16, 2, 4, [1, 1, 1], [1, 300, 17], 0),
+    (128, 64, 1, 8, [1, 1], [129, 64], 0),
+    (128, 128, 3, 1, [1, 1, 1, 1], [5, 1000, 16, 15], 0),
+    (64, 32, 2, 3, [4, 1, 5], [40, 333, 5], 0),
+    (64, 16, 1, 7, [2, 3], [700, 48], 100),
+    (128, 16, 1, 16, [1, 2], [260, 31], 0),
+    (128, 32, 2, 5, [3, 1], [90, 257], 33),
+    (64, 64, 2, 4, [1] * 9, [9, 1, 2, 900, 64, 65, 63, 31, 33], 0),
+])
+def test_attention_single_tokens(dim, page, heads, group, q_len, kv_len, window):
+    pages, n = _paged(kv_len, page, 3)
+    cache, ref = _random_cache(n, page, heads, dim, 5, gap=1)
+    cu = [0] + np.cumsum(q_len).tolist()
+    _check(cache, ref, _queries(cu[-1], heads * group, dim, 7, 2.0), cu, pages, kv_len, window=window)
+
+
+# prompts: lengths around the tiles' borders, a history, windows, a query longer than its keys
+@pytest.mark.parametrize("dim,page,heads,group,q_len,kv_len,window,causal", [
+    (128, 16, 1, 4, [130, 1, 64], [130, 40, 200], 0, True),
+    (64, 64, 2, 1, [200], [200], 0, True),
+    (128, 32, 1, 3, [45, 97], [333, 97], 50, True),
+    (64, 16, 1, 5, [77, 0, 31], [256, 10, 31], 0, True),
+    (64, 128, 2, 2, [40, 70, 33], [129, 0, 500], 0, False),
+    (128, 64, 1, 1, [257], [255], 0, True),
+    (64, 32, 1, 8, [60, 17], [30, 0], 0, True),
+    (128, 16, 1, 1, [300], [383], 128, True),
+])
+def test_attention_prompts(dim, page, heads, group, q_len, kv_len, window, causal):
+    pages, n = _paged(kv_len, page, 4)
+    cache, ref = _random_cache(n, page, heads, dim, 6)
+    cu = [0] + np.cumsum(q_len).tolist()
+    _check(cache, ref, _queries(cu[-1], heads * group, dim, 8, 2.0), cu, pages, kv_len, window=window, causal=causal)
+
+
+@pytest.mark.parametrize("max_q", [1, 200])
+def test_attention_leaves_other_rows_and_nan_stays_in_its_row(max_q):
+    dev = require_gpu()
+    kv_len, cu = [70, 0, 33], [2, 3, 5, 45]
+    pages, n = _paged(kv_len, 16, 9)
+    cache, ref = _random_cache(n, 16, 2, 64, 10)
+    # what lies behind the last token of a page is garbage: NaN scales
+    for b, m in enumerate(kv_len):
+        if m % 16:
+            for t in (cache.k_scales, cache.v_scales, cache.k_codes, cache.v_codes):
+                t[int(pages[b, m // 16]), :, m % 16:] = 0xFF
+    q = _queries(50, 4, 64, 11)
+    out = torch.full((50, 4, 64), 3.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((50, 4), 3.0, device=dev)
+    _check(cache, ref, q, cu, pages, kv_len, out=out, lse=lse, max_q=max_q)
+    edge = [0, 1, 45, 46, 47, 48, 49]
+    assert bool((out[edge] == 3.0).all()) and bool((lse[edge] == 3.0).all())
+    clean = out.clone()
+    q[7, 1, 5] = math.nan
+    q[9, 3, 0] = math.inf
+    got = F.kv_attention(cache, q.to(dev), torch.tensor(cu, dtype=I32, device=dev),
+                         torch.from_numpy(pages).to(dev), torch.tensor(kv_len, dtype=I32, device=dev), max_q,
+                         out=out.clone())
+    # queries 7 and 9 of the last sequence see no key (33 keys, 40 queries): masked, so zeros; 30 sees some
+    assert torch.equal(got, clean)
+    q[30, 1, 5] = math.nan
+    q[31, 3, 0] = -math.inf
+    got = F.kv_attention(cache, q.to(dev), torch.tensor(cu, dtype=I32, device=dev),
+                         torch.from_numpy(pages).to(dev), torch.tensor(kv_len, dtype=I32, device=dev), max_q,
+                         out=out.clone())
+    assert bool(got[30, 1].isnan().all()) and bool(got[31, 3].isnan().all())
+    got[30, 1], got[31, 3] = clean[30, 1], clean[31, 3]
+    assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("max_q", [1, 100])
+def test_attention_reports_bad_pages_and_lengths(max_q):
+    dev = require_gpu()
+    cache, ref = _random_cache(4, 16, 1, 64, 12)
+    q = _queries(3, 2, 64, 13)
+    pages = np.array([[0, 1], [2, 99], [3, -7]], np.int32)
+    cu = [0, 1, 2, 3]
+
+    def run(pages, kv_len, cu):
+        status = torch.zeros(1, dtype=I32, device=dev)
+        out = F.kv_attention(cache, q.to(dev), torch.tensor(cu, dtype=I32, device=dev),
+                             torch.from_numpy(pages).to(dev), torch.tensor(kv_len, dtype=I32, device=dev), max_q,
+                             status=status, out=torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=dev))
+        return out, int(status)
+
+    good, ok = run(pages, [32, 16, 16], cu)
+    assert ok == 0
+    out, bad = run(pages, [32, 20, 16], cu)     # page 99 holds visible tokens: they do not count
+    assert bad == F.STATUS_INDEX and torch.equal(out, good)
+    out, bad = run(pages, [32, 16, 32], cu)
+    assert bad == F.STATUS_INDEX and torch.equal(out, good)
+    out, bad = run(pages, [33, 16, -1], cu)     # clamped to the table, and to nothing
+    assert bad == F.STATUS_INDEX and torch.equal(out[:2], good[:2]) and not out[2].any()
+    for broken in ([0, 1, 4, 3], [0, 1, 0, 3], [-1, 1, 2, 3], [0, 1, 2, 9]):
+        out, bad = run(pages, [32, 16, 16], broken)
+        assert bad & F.STATUS_INDEX and bool(out.isfinite().all())
+
+
+def test_attention_of_extreme_values():
+    """Scores far apart, a dominant late key, tiny and huge queries, a zero query and zero scales."""
+    dev = require_gpu()
+    kv_len = [400]
+    pages, n = _paged(kv_len, 16, 20)
+    cache, ref = _random_cache(n, 16, 1, 128, 21)
+    q = _queries(6, 8, 128, 22)
+    q[0] *= 60.0
+    q[1] *= 2.0 ** -100
+    q[2] = 0
+    q[3, :, ::2] *= 2.0 ** -30
+    _check(cache, ref, q, [0, 6], pages, kv_len)
+    _check(cache, ref, q[4:], [0, 2], pages, kv_len, scale=-0.3)
+    _check(cache, ref, q[4:], [0, 2], pages, kv_len, scale=0.0)
+
+
+def test_same_call_same_bits_and_another_stream():
+    dev = require_gpu()
+    kv_len, cu = [900, 33, 410], [0, 1, 2, 3]
+    pages, n = _paged(kv_len, 16, 30)
+    cache, _ = _random_cache(n, 16, 2, 128, 31)
+    q = _queries(3, 8, 128, 32).to(dev)
+    args = (cache, q, torch.tensor(cu, dtype=I32, device=dev), torch.from_numpy(pages).to(dev),
+            torch.tensor(kv_len, dtype=I32, device=dev), 1)
+    a = F.kv_attention(*args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [F.kv_attention(*args, stream=side) for _ in range(3)] + [F.kv_attention(*args) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, x) for x in got)
+
+
+def test_decoding_steps_captured_and_replayed():
+    """Append and attention of a growing batch, captured once and replayed:
+    every step equals the same calls made outside a graph, and the last one
+    the 64-bit computation."""
+    dev = require_gpu()
+    B, H, HQ, D, P = 3, 2, 8, 128, 16
+    start, steps = [14, 0, 47], 4
+    pages = np.array([[3, 1, 9, 8], [0, 6, 7, 2], [4, 10, 5, 11]], np.int32)
+    cu = torch.arange(B + 1, dtype=I32, device=dev)
+    pd, table = torch.from_numpy(pages).to(dev), _table(100, D).to(dev)
+    g = torch.Generator().manual_seed(40)
+    x = torch.randn(steps, B, HQ + 2 * H, D, generator=g).to(torch.bfloat16).to(dev)
+
+    def make():
+        c, ref = _random_cache(12, P, H, D, 41)
+        buf = {"x": torch.zeros_like(x[0]), "len": torch.tensor(start, dtype=I32, device=dev),
+               "y": torch.zeros(B, HQ, D, dtype=torch.bfloat16, device=dev)}
+        return c, buf
+
+    def step(c, buf):
+        pos = buf["len"].clone()
+        at = pos.long()
+        slots = pd.long().gather(1, (at // P)[:, None]).squeeze(1) * P + at % P
+        q = F.kv_append(c, buf["x"][:, HQ:HQ + H], buf["x"][:, HQ + H:], slots, pos, table, q=buf["x"][:, :HQ])
+        buf["len"] += 1
+        F.kv_attention(c, q, cu, pd, buf["len"], 1, out=buf["y"])
+        return q
+
+    eager, be = make()
+    want = []
+    for i in range(steps):
+        be["x"].copy_(x[i])
+        q_last = step(eager, be)
+        want.append(be["y"].clone())
+    c, buf = make()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*make())                     # warm up outside the capture, on other buffers
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(c, buf)
+    buf["len"].copy_(torch.tensor(start, dtype=I32))
+    for i in range(steps):
+        buf["x"].copy_(x[i])
+        graph.replay()
+        assert torch.equal(buf["y"], want[i]), i
+    for a, b in ((c.k_codes, eager.k_codes), (c.v_scales, eager.v_scales)):
+        assert torch.equal(a, b)
+    np_ = lambda t: t.cpu().numpy()  # noqa: E731
+    out, _, bound, _ = R.attention(q_last.cpu(), np_(c.k_codes), np_(c.k_scales), np_(c.v_codes), np_(c.v_scales),
+                                   np_(c.k_tensor_scale), np_(c.v_tensor_scale), [0, 1, 2, 3], pages,
+                                   [m + steps for m in start], True, 0, 1 / math.sqrt(D))
+    assert (np.abs(np_(want[-1].double()) - out) <= bound).all()
+
+
+def test_prompt_and_then_tokens_agree():
+    """A prompt appended and attended in one call, and token by token, over
+    the same cache: the same keys, so the same answers within both bounds."""
+    dev = require_gpu()
+    T, H, HQ, D, P = 75, 1, 4, 64, 32
+    g = torch.Generator().manual_seed(50)
+    x = torch.randn(T, HQ + 2 * H, D, generator=g).to(torch.bfloat16).to(dev)
+    table = _table(T, D).to(dev)
+    pages = torch.tensor([[2, 0, 1]], dtype=I32, device=dev)
+    pos = torch.arange(T, dtype=I32, device=dev)
+    slots = pages[0].long()[pos.long() // P] * P + pos.long() % P
+    cache = F.KVCache.empty(3, P, H, D, 5.0, 5.0, device=dev)
+    q = F.kv_append(cache, x[:, HQ:HQ + H], x[:, HQ + H:], slots, pos, table, q=x[:, :HQ])
+    whole = F.kv_attention(cache, q, torch.tensor([0, T], dtype=I32, device=dev), pages,
+                           torch.tensor([T], dtype=I32, device=dev), T)
+    other = F.KVCache.empty(3, P, H, D, 5.0, 5.0, device=dev)
+    rows, qs = [], []
+    for i in range(T):
+        s = slice(i, i + 1)
+        qs.append(F.kv_append(other, x[s, HQ:HQ + H], x[s, HQ + H:], slots[s], pos[s], table, q=x[s, :HQ]))
+        rows.append(F.kv_attention(other, qs[-1], torch.tensor([0, 1], dtype=I32, device=dev), pages,
+                                   torch.tensor([i + 1], dtype=I32, device=dev), 1))
+    assert torch.equal(torch.cat(qs), q)
+    np_ = lambda t: t.cpu().numpy()  # noqa: E731
+    out, _, bound, _ = R.attention(q.cpu(), np_(cache.k_codes), np_(cache.k_scales), np_(cache.v_codes),
+                                   np_(cache.v_scales), np_(cache.k_tensor_scale), np_(cache.v_tensor_scale),
+                                   [0, T], np_(pages), [T], True, 0, 1 / 8)
+    for got in (whole, torch.cat(rows)):
+        assert (np.abs(np_(got.double()) - out) <= bound).all()
+
+
+def test_empty_calls():
+    dev = require_gpu()
+    cache = F.KVCache.empty(1, 16, 1, 64, 1.0, 1.0, device=dev)
+    none = torch.empty(0, 1, 64, dtype=torch.bfloat16, device=dev)
+    assert F.kv_append(cache, none, none, torch.empty(0, dtype=torch.int64, device=dev)) is None
+    k, v = F.kv_read(cache, torch.empty(0, dtype=torch.int64, device=dev))
+    assert k.shape == v.shape == (0, 1, 64)
+    zero = torch.zeros(1, dtype=I32, device=dev)
+    out = F.kv_attention(cache, none, zero, torch.empty(0, 3, dtype=I32, device=dev), zero[:0], 0)
+    assert out.shape == (0, 1, 64)
+    # a table without columns: no keys
+    one = torch.ones(1, 1, 64, dtype=torch.bfloat16, device=dev)
+    out, lse = F.kv_attention(cache, one, torch.tensor([0, 1], dtype=I32, device=dev),
+                              torch.empty(1, 0, dtype=I32, device=dev), zero, 1, return_lse=True)
+    assert not out.any() and bool(torch.isneginf(lse).all())
