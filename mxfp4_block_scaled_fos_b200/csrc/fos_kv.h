@@ -59,5 +59,9 @@ struct KvAttnArgs {
 cudaError_t launch_kv_append(const KvAppendArgs& a, int fmt, bool interleaved, cudaStream_t st);
 cudaError_t launch_kv_read(const KvReadArgs& a, cudaStream_t st);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, cudaStream_t st);
+// rows: the largest number of rows (queries times heads of a group) of a
+// sequence; it chooses the row tile
+size_t kv_decode_workspace_bytes(int dim, int rows);
+cudaError_t launch_kv_decode(const KvAttnArgs& a, int rows, float* part, cudaStream_t st);
 
 }  // namespace fos

@@ -122,12 +122,9 @@ fos_status fos_kv_read(const fos_kv_cache* cache, const int64_t* slots, int64_t 
 
 size_t fos_kv_attention_workspace_size(const fos_kv_cache* cache, int64_t total_q, int64_t batch, int64_t q_heads,
                                        int64_t max_q) {
-  (void)cache;
-  (void)total_q;
-  (void)batch;
-  (void)q_heads;
-  (void)max_q;
-  return 0;
+  if (!cache || cache->heads < 1 || total_q < 1 || batch < 1) return 0;
+  const int64_t rows = max_q * (q_heads / cache->heads);
+  return kv_decode_workspace_bytes((int)cache->head_dim, rows > 16 ? 16 : (int)rows);
 }
 
 fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_ld, int64_t total_q,
@@ -172,7 +169,11 @@ fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_
   a.window = window;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = status;
-  return launch_kv_attention(a, (cudaStream_t)stream) == cudaSuccess ? FOS_OK : FOS_ERR_CUDA;
+  const int64_t rows = max_q * a.group;
+  const cudaError_t ce = rows <= 64 ? launch_kv_decode(a, rows > 16 ? 16 : (int)rows, (float*)workspace,
+                                                       (cudaStream_t)stream)
+                                    : launch_kv_attention(a, (cudaStream_t)stream);
+  return ce == cudaSuccess ? FOS_OK : FOS_ERR_CUDA;
 }
 
 }  // extern "C"
