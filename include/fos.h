@@ -433,7 +433,7 @@ fos_status fos_kv_read(const fos_kv_cache* cache, const int64_t* slots, int64_t 
  * The work is split by the lengths alone: the same call gives the same bits.
  */
 size_t fos_kv_attention_workspace_size(const fos_kv_cache* cache, int64_t total_q, int64_t batch, int64_t q_heads,
-                                       int64_t max_q);
+                                       int64_t max_q, int64_t max_pages);
 fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_ld, int64_t total_q,
                             int64_t q_heads, const int32_t* cu_q, int64_t batch, const int32_t* pages,
                             int64_t max_pages, const int32_t* kv_len, int64_t max_q, float scale, int32_t causal,

@@ -48,6 +48,28 @@ fos_status check_rows(const void* x, int64_t ld, int64_t heads, int64_t dim) {
   return FOS_OK;
 }
 
+// Which kernel a call of fos_kv_attention runs, from what the host knows.
+struct AttnPlan {
+  bool prompt;
+  int rows, splits;
+  size_t bytes;
+};
+
+AttnPlan attn_plan(const fos_kv_cache* c, int64_t total_q, int64_t batch, int64_t q_heads, int64_t max_q,
+                   int64_t max_kv) {
+  AttnPlan p{};
+  const int64_t group = q_heads / c->heads, rows = max_q * group;
+  p.prompt = rows > 64;
+  if (p.prompt) {
+    p.splits = kv_prompt_splits(total_q, batch, group, c->heads, max_kv);
+    p.bytes = kv_prompt_workspace_bytes((int)c->head_dim, p.splits, total_q * q_heads);
+  } else {
+    p.rows = rows > 16 ? 16 : (int)rows;
+    p.bytes = kv_decode_workspace_bytes((int)c->head_dim, p.rows);
+  }
+  return p;
+}
+
 }  // namespace
 }  // namespace fos
 
@@ -121,10 +143,10 @@ fos_status fos_kv_read(const fos_kv_cache* cache, const int64_t* slots, int64_t 
 }
 
 size_t fos_kv_attention_workspace_size(const fos_kv_cache* cache, int64_t total_q, int64_t batch, int64_t q_heads,
-                                       int64_t max_q) {
-  if (!cache || cache->heads < 1 || total_q < 1 || batch < 1) return 0;
-  const int64_t rows = max_q * (q_heads / cache->heads);
-  return kv_decode_workspace_bytes((int)cache->head_dim, rows > 16 ? 16 : (int)rows);
+                                       int64_t max_q, int64_t max_pages) {
+  if (!cache || cache->heads < 1 || q_heads < cache->heads || total_q < 1 || batch < 1 || max_q < 0 || max_pages < 0)
+    return 0;
+  return attn_plan(cache, total_q, batch, q_heads, max_q, max_pages * cache->page_size).bytes;
 }
 
 fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_ld, int64_t total_q,
@@ -136,7 +158,8 @@ fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_
   fos_status e = check_pool(cache, &a.p);
   if (e != FOS_OK) return e;
   if (causal != 0 && causal != 1) return FOS_ERR_ARG;
-  if (window < 0 || (window && !causal) || max_q < 0 || !isfinite(scale)) return FOS_ERR_ARG;
+  if (window < 0 || (window && !causal) || max_q < 0 || max_q > (1 << 30) || !isfinite(scale))
+    return FOS_ERR_ARG;
   if (total_q < 0 || total_q > (1 << 30) || batch < 0 || batch > (1 << 20) || max_pages < 0) return FOS_ERR_SHAPE;
   if (q_heads < 1 || q_heads > 65536 || q_heads % a.p.heads) return FOS_ERR_SHAPE;
   if (total_q * (q_heads / a.p.heads) >= (1ll << 31) || max_pages * cache->page_size >= (1ll << 31))
@@ -147,9 +170,9 @@ fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_
   if ((e = check_rows(out, out_ld, q_heads, a.p.dim)) != FOS_OK) return e;
   if (!aligned(cu_q, 4) || !aligned(pages, 4) || !aligned(kv_len, 4) || (lse && !aligned(lse, 4)))
     return FOS_ERR_ALIGN;
-  const size_t need = fos_kv_attention_workspace_size(cache, total_q, batch, q_heads, max_q);
-  if (need) {
-    if (!workspace || workspace_bytes < need) return FOS_ERR_WORKSPACE;
+  const AttnPlan plan = attn_plan(cache, total_q, batch, q_heads, max_q, max_pages * cache->page_size);
+  if (plan.bytes) {
+    if (!workspace || workspace_bytes < plan.bytes) return FOS_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return FOS_ERR_ALIGN;
   }
   a.q = (const uint16_t*)q;
@@ -169,10 +192,8 @@ fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_
   a.window = window;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = status;
-  const int64_t rows = max_q * a.group;
-  const cudaError_t ce = rows <= 64 ? launch_kv_decode(a, rows > 16 ? 16 : (int)rows, (float*)workspace,
-                                                       (cudaStream_t)stream)
-                                    : launch_kv_attention(a, (cudaStream_t)stream);
+  const cudaError_t ce = plan.prompt ? launch_kv_prompt(a, plan.splits, (float*)workspace, (cudaStream_t)stream)
+                                     : launch_kv_decode(a, plan.rows, (float*)workspace, (cudaStream_t)stream);
   return ce == cudaSuccess ? FOS_OK : FOS_ERR_CUDA;
 }
 

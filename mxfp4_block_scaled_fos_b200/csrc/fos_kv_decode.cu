@@ -26,15 +26,11 @@
 //    free: lane (g, c) takes 16 or 32 consecutive values of tokens g, g + 8.
 //  - For V^T a register holds one value of two tokens: nibbles of two
 //    tokens' words are zipped into bytes before the conversion.
-//  - Queries are scaled by a power of two for each row to below 2^15: exact
-//    in f16 for values down to 2^-39 of the row's largest.
-// The running maximum m of a row is only raised (and the sums rescaled) when
-// a score passes it by 2^8; weights are 2^(x - m + 6), at most 2^14, rounded
-// to f16 (2^-11 relative down to 2^-20 of the largest, 2^-31 absolute).
+// The running maximum of a row is raised, and its sums rescaled, only when a
+// score passes it by 2^8 (fos_kv.cuh).
 #include <math_constants.h>
 
-#include "fos_device.cuh"
-#include "fos_kv.h"
+#include "fos_kv.cuh"
 
 namespace fos {
 namespace {
@@ -43,7 +39,6 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kSlice = 16, kTile = kSlice * kWarps;   // tokens
 constexpr int kStages = 4;
 constexpr int kMaxCtas = 320;                         // shares: two CTAs on each of up to 160 SMs
-constexpr float kLift = 6.0f, kSlack = 8.0f;          // log2
 constexpr uint32_t kWaitLimit = 1u << 22;
 
 template <int D, int NT>
@@ -61,8 +56,6 @@ struct Cfg {
   static constexpr int kSmem = kOffPlan + 64 + kWarps * 8;
   static constexpr int kPart = kRows * (D + 2);                          // floats of one partial result
 };
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   for (uint32_t it = 0; it < kWaitLimit; ++it) {
@@ -96,36 +89,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return d;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// byte j of w: two codes -> f16x2
-template <int J>
-__device__ __forceinline__ uint32_t codes_h2(uint32_t w) {
-  return e2m1x2_to_h2(__byte_perm(w, 0u, 0x4440u + J));
-}
-
-// two E4M3 bytes -> f16x2
-__device__ __forceinline__ uint32_t scales_h2(uint32_t w16) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)w16));
-  return h;
-}
-
 // The token of A row r of a slice: lane c's V tokens (rows 2c, 2c + 1,
 // 2c + 8, 2c + 9) are c of each group of four, and neighbouring rows differ
 // in parity, which spreads both products' shared-memory reads over the banks.
@@ -140,14 +103,6 @@ struct Span {
   int lo, hi, base, tiles;
 };
 
-__device__ __forceinline__ int query_hi(const KvAttnArgs& a, int n, int len, int i) {
-  return a.causal ? max(0, len - n + i + 1) : len;
-}
-
-__device__ __forceinline__ int query_lo(const KvAttnArgs& a, int hi) {
-  return a.window && hi > a.window ? (int)(hi - a.window) : 0;
-}
-
 template <int ROWS>
 __device__ __forceinline__ Span span_of(const KvAttnArgs& a, int n, int len, int rt) {
   Span s;
@@ -157,17 +112,6 @@ __device__ __forceinline__ Span span_of(const KvAttnArgs& a, int n, int len, int
   s.base = s.lo & ~(kSlice - 1);
   s.tiles = max(1, (s.hi - s.base + kTile - 1) / kTile);
   return s;
-}
-
-// Queries and keys of sequence b, clamped to what the arguments allow.
-__device__ __forceinline__ void lengths_of(const KvAttnArgs& a, int b, int& q0, int& n, int& len, bool& bad) {
-  const int x = a.cu_q[b], y = a.cu_q[b + 1];
-  const long long cap = a.max_pages << a.p.page_shift;
-  const int m = a.kv_len[b];
-  bad = x < 0 || y < x || y > a.total_q || m < 0 || m > cap;
-  q0 = x;
-  n = (x < 0 || y < x || y > a.total_q) ? 0 : y - x;
-  len = max(0, (int)min((long long)m, cap));
 }
 
 template <int ROWS>
@@ -389,18 +333,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_decode(const KvAttnArgs a, f
       for (int k = 0; k < LD; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
       top = max(top, __shfl_xor_sync(~0u, top, 1));
       top = max(top, __shfl_xor_sync(~0u, top, 2));
-      const bool finite = top < 0x7f800000u;
-      // 2^(14 - exponent) in two factors, so that neither leaves the normal range
-      const int e = top == 0 ? 14 : max((int)(top >> 23), 1) - 127;
-      const int up = 14 - e, u1 = up / 2, u2 = up - u1;
-      const float f1 = __uint_as_float((uint32_t)(127 + u1) << 23), f2 = __uint_as_float((uint32_t)(127 + u2) << 23);
-      const float d1 = __uint_as_float((uint32_t)(127 - u1) << 23), d2 = __uint_as_float((uint32_t)(127 - u2) << 23);
-      const float mine = finite ? base_scale * d1 * d2 : CUDART_NAN_F;
+      const RowScale sc = row_scale(top);
+      const float mine = sc.finite ? base_scale * sc.down1 * sc.down2 : CUDART_NAN_F;
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2)
-          qf[nt][k][e2] = finite ? pack_h2(v[4 * k + 2 * e2] * f1 * f2, v[4 * k + 2 * e2 + 1] * f1 * f2) : 0u;
+          qf[nt][k][e2] = sc.finite ? pack_h2(v[4 * k + 2 * e2] * sc.up1 * sc.up2, v[4 * k + 2 * e2 + 1] * sc.up1 * sc.up2)
+                                    : 0u;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         rs[nt][k] = __shfl_sync(~0u, mine, (2 * c + k) * 4);

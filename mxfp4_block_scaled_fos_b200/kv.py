@@ -52,7 +52,7 @@ def _lib():
         L.fos_kv_read.restype = _I32
         L.fos_kv_read.argtypes = [CP, _P, _I64, _P, _P, _P, _P]
         L.fos_kv_attention_workspace_size.restype = sz
-        L.fos_kv_attention_workspace_size.argtypes = [CP, _I64, _I64, _I64, _I64]
+        L.fos_kv_attention_workspace_size.argtypes = [CP, _I64, _I64, _I64, _I64, _I64]
         L.fos_kv_attention.restype = _I32
         L.fos_kv_attention.argtypes = [CP, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, ctypes.c_float, _I32,
                                        _I64, _P, _I64, _P, _P, sz, _P, _P]
@@ -228,9 +228,10 @@ def kv_read(cache: KVCache, slots: torch.Tensor, out: Optional[Tuple[torch.Tenso
     return out[0], out[1]
 
 
-def kv_attention_workspace_size(cache: KVCache, total_q: int, batch: int, q_heads: int, max_q: int) -> int:
+def kv_attention_workspace_size(cache: KVCache, total_q: int, batch: int, q_heads: int, max_q: int,
+                                max_pages: int) -> int:
     """Bytes of workspace kv_attention needs."""
-    return int(_lib().fos_kv_attention_workspace_size(cache._ref, total_q, batch, q_heads, max_q))
+    return int(_lib().fos_kv_attention_workspace_size(cache._ref, total_q, batch, q_heads, max_q, max_pages))
 
 
 def kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, pages: torch.Tensor, kv_len: torch.Tensor,
@@ -269,7 +270,7 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, pages: tor
         lse = torch.empty(t, hq, dtype=torch.float32, device=q.device)
     with _on(cache.device, stream) as s:
         L = _lib()
-        need = L.fos_kv_attention_workspace_size(cache._ref, t, b, hq, max_q)
+        need = L.fos_kv_attention_workspace_size(cache._ref, t, b, hq, max_q, pages.shape[1])
         if workspace is None and need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
             if stream is not None:

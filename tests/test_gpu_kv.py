@@ -202,6 +202,10 @@ def test_attention_single_tokens(dim, page, heads, group, q_len, kv_len, window)
     (128, 64, 1, 1, [257], [255], 0, True),
     (64, 32, 1, 8, [60, 17], [30, 0], 0, True),
     (128, 16, 1, 1, [300], [383], 128, True),
+    # long enough for several CTAs to share a row tile's tokens; one of the sequences is short, one empty
+    (128, 64, 1, 2, [70, 3, 40], [2300, 5, 0], 0, True),
+    (64, 16, 1, 3, [100], [1700], 600, True),
+    (128, 128, 1, 1, [90, 66], [1290, 700], 0, False),
 ])
 def test_attention_prompts(dim, page, heads, group, q_len, kv_len, window, causal):
     pages, n = _paged(kv_len, page, 4)
@@ -273,7 +277,8 @@ def test_attention_reports_bad_pages_and_lengths(max_q):
         assert bad & F.STATUS_INDEX and bool(out.isfinite().all())
 
 
-def test_attention_of_extreme_values():
+@pytest.mark.parametrize("max_q", [1, 100])
+def test_attention_of_extreme_values(max_q):
     """Scores far apart, a dominant late key, tiny and huge queries, a zero query and zero scales."""
     dev = require_gpu()
     kv_len = [400]
@@ -284,9 +289,9 @@ def test_attention_of_extreme_values():
     q[1] *= 2.0 ** -100
     q[2] = 0
     q[3, :, ::2] *= 2.0 ** -30
-    _check(cache, ref, q, [0, 6], pages, kv_len)
-    _check(cache, ref, q[4:], [0, 2], pages, kv_len, scale=-0.3)
-    _check(cache, ref, q[4:], [0, 2], pages, kv_len, scale=0.0)
+    _check(cache, ref, q, [0, 6], pages, kv_len, max_q=max_q)
+    _check(cache, ref, q[4:], [0, 2], pages, kv_len, scale=-0.3, max_q=max_q)
+    _check(cache, ref, q[4:], [0, 2], pages, kv_len, scale=0.0, max_q=max_q)
 
 
 def test_same_call_same_bits_and_another_stream():
