@@ -31,10 +31,19 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// byte j of w: two codes -> f16x2
-template <int J>
-__device__ __forceinline__ uint32_t codes_h2(uint32_t w) {
-  return e2m1x2_to_h2(__byte_perm(w, 0u, 0x4440u + J));
+// The 8 codes of a word -> four f16x2 (value 2j in the low half of h[j]).
+// Split in one move, each conversion takes its byte out of the word by
+// itself; with a byte permute for each (e2m1x2_to_h2) 47 codes a cycle and SM
+// against 72.  tests/test_gpu_kv.py compares every byte in every place.
+__device__ __forceinline__ void codes_h2x4(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 }
 
 // two E4M3 bytes -> f16x2

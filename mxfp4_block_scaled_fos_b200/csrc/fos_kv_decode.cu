@@ -12,20 +12,26 @@
 // unnormalised output) in the workspace and k_kv_join adds them in the order
 // of the tokens.
 //
-// Inside a CTA each of 8 warps takes 16 tokens of a tile (a slice), which
-// lie in one page, with softmax statistics and a ring of bulk copies of its
-// own: no barrier until the end of an item.  The products run on m16n8k16
-// with f16 operands and f32 sums:
-//   S^T = K Q^T      A = 16 tokens of keys, B = 8 rows of queries
-//   O^T += V^T P^T   A = 16 output values, B = the weights of 8 rows
-// so that 8 rows fill an MMA and no operand goes through shared memory:
-//  - An E2M1 code times its E4M3 scale has 6 significant bits between 2^-10
-//    and 2688: exact in f16.  Codes are converted two at a time
-//    (cvt f16x2.e2m1x2) and multiplied by their scale.
-//  - The order of the head's values along the first product's reduction is
-//    free: lane (g, c) takes 16 or 32 consecutive values of tokens g, g + 8.
-//  - For V^T a register holds one value of two tokens: nibbles of two
-//    tokens' words are zipped into bytes before the conversion.
+// A CTA has two groups of 4 warps, which take its tiles in turn; a warp has
+// 32 tokens of a tile.
+//   S^T = K Q^T runs on the FP4 tensor cores (tcgen05 kind::mxf4nvf4) on the
+// codes and scales as the cache holds them: the 128 tokens are the rows of A.
+// Queries become FP4 operands without loss that counts: a row is scaled by a
+// power of two to integers below 2^23 (24 bits below the row's largest
+// value), written in balanced base 8, and the digits -4 .. 4 are E2M1 values
+// (halves). Digit j and digit j + 4 share column j of a row, as two products
+// with scales 2^-6 and 2^6; a score is the sum of its 4 columns times 8^j.
+// Nothing of a key is converted in registers, where the conversion bounded an
+// earlier version: e2m1 conversions run at 16 values pairs a cycle.
+//   O^T += V^T P^T runs on m16n8k16 with f16 operands: A = 16 output values
+// of 16 tokens, B = the weights of 8 rows. A code times its E4M3 scale has 6
+// significant bits between 2^-10 and 2688, exact in f16. A register holds one
+// value of two tokens: nibbles of two tokens' words are zipped into bytes and
+// converted together (cvt f16x2.e2m1x2). A warp reads the scores of its own
+// tokens, a token for each lane, and only its own values, so warps of a group
+// meet once a tile: to hand over the next tile's key scales and to know that
+// the scores have been read.
+// The next tile's scores are computed while this one's values are.
 // The running maximum of a row is raised, and its sums rescaled, only when a
 // score passes it by 2^8 (fos_kv.cuh).
 #include <math_constants.h>
@@ -36,25 +42,36 @@ namespace fos {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kSlice = 16, kTile = kSlice * kWarps;   // tokens
-constexpr int kStages = 4;
+constexpr int kSlice = 16, kTile = 128;               // tokens of one copy, of a tile
+constexpr int kStagesK = 2, kStagesV = 3;             // tiles of a group in shared memory
 constexpr int kMaxCtas = 320;                         // shares: two CTAs on each of up to 160 SMs
-constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr float kNone = -1e30f;                       // the maximum of a row that has seen nothing
+constexpr uint32_t kWaitLimit = 1u << 20;
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kCodes = kSlice * D / 2, kScales = kSlice * D / 16;
-  static constexpr int kStage = 2 * (kCodes + kScales);
-  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kCols = 4 * kRows;                                // score columns: row r, digits j: j * kRows + r
+  static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16; // bytes of a tile's keys (or values)
+  static constexpr int kTile1 = kCodes + kScales;
+  static constexpr int kGroup = (kStagesK + kStagesV) * kTile1;
   static constexpr int kLdO = D + 4;                                     // floats
-  static constexpr int kMerge = kWarps * kRows * kLdO * 4;               // the warps' outputs, over the ring
-  static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kOffStat = kBody;                                 // m, l [warps][rows]
-  static constexpr int kOffBar = kOffStat + 2 * kWarps * kRows * 4;
-  static constexpr int kOffPlan = kOffBar + kWarps * kStages * 8;
-  static constexpr int kSmem = kOffPlan + 64 + kWarps * 8;
+  static constexpr int kMerge = kWarps * kRows * kLdO * 4;               // the warps' outputs, over the stages
+  static constexpr int kOffQ = 2 * kGroup > kMerge ? 2 * kGroup : (kMerge + 1023) / 1024 * 1024;
+  static constexpr int kQ = kCols * D / 2;                               // one set of digits
+  static constexpr int kOffP = kOffQ + 2 * kQ;                           // weights, [warp][32 tokens][rows] f16
+  static constexpr int kOffStat = kOffP + kWarps * 32 * kRows * 2;       // m, l [warps][rows]
+  static constexpr int kOffRow = kOffStat + 2 * kWarps * kRows * 4;      // rs, hi, lo [rows]
+  static constexpr int kOffBar = kOffRow + 3 * kRows * 4;                // a group's scores are there
+  static constexpr int kOffPlan = kOffBar + 2 * 8 + 16;
+  static constexpr int kSmem = kOffPlan + 64 + kWarps * 8 + 1024;        // + alignment slack
   static constexpr int kPart = kRows * (D + 2);                          // floats of one partial result
+  static constexpr uint32_t kTmemCols = NT == 1 ? 128 : 256;
+  static constexpr uint32_t kColSFA = 2 * kCols, kColSFB = kColSFA + 16; // + 8 * group; 4 each for both digit sets
+  // kind::mxf4nvf4, E2M1, K-major, E4M3 scales, M = 128, N = kCols
+  static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(kCols >> 3) << 17) | ((128u >> 4) << 24);
+  static_assert(kColSFB + 8 <= kTmemCols, "tensor memory");
+  static_assert(kSmem <= 113 * 1024, "two CTAs on an SM");
 };
 
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
@@ -70,9 +87,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   return false;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+// Copies straight to shared memory, 16 or 4 bytes.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -83,15 +103,57 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
-  uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
-  return d;
+__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                     uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) : "memory");
 }
 
-// The token of A row r of a slice: lane c's V tokens (rows 2c, 2c + 1,
-// 2c + 8, 2c + 9) are c of each group of four, and neighbouring rows differ
-// in parity, which spreads both products' shared-memory reads over the banks.
+// K-major operand whose rows are D / 2 bytes, swizzled over that width: 64
+// bytes (D = 128) or 32; 8-row groups follow one another.
+template <int D>
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(8 * (D / 2) >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)(D == 128 ? 4 : 6) << 61);
+}
+
+// A 512-byte scale atom (32 rows of 16 bytes, no swizzle) as a copy source.
+__device__ __forceinline__ uint64_t desc_sf(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+// Byte b of row n of such an operand: the swizzle exchanges 16-byte chunks.
+template <int D>
+__device__ __forceinline__ int row_chunk(int n) {
+  return D == 128 ? (n >> 1) & 3 : (n >> 2) & 1;
+}
+template <int D>
+__device__ __forceinline__ int row_at(int n, int b) {
+  return n * (D / 2) + (((b >> 4) ^ row_chunk<D>(n)) << 4) + (b & 15);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
+  static_assert(N % 32 == 0, "");
+#pragma unroll
+  for (int k = 0; k < N; k += 32)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+        "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[k]), "=r"(r[k + 1]), "=r"(r[k + 2]), "=r"(r[k + 3]), "=r"(r[k + 4]), "=r"(r[k + 5]), "=r"(r[k + 6]),
+          "=r"(r[k + 7]), "=r"(r[k + 8]), "=r"(r[k + 9]), "=r"(r[k + 10]), "=r"(r[k + 11]), "=r"(r[k + 12]),
+          "=r"(r[k + 13]), "=r"(r[k + 14]), "=r"(r[k + 15]), "=r"(r[k + 16]), "=r"(r[k + 17]), "=r"(r[k + 18]),
+          "=r"(r[k + 19]), "=r"(r[k + 20]), "=r"(r[k + 21]), "=r"(r[k + 22]), "=r"(r[k + 23]), "=r"(r[k + 24]),
+          "=r"(r[k + 25]), "=r"(r[k + 26]), "=r"(r[k + 27]), "=r"(r[k + 28]), "=r"(r[k + 29]), "=r"(r[k + 30]),
+          "=r"(r[k + 31])
+        : "r"(addr + k));
+}
+
+// The token of index r of the second product's 16 tokens: lane c's tokens
+// (2c, 2c + 1, 2c + 8, 2c + 9) are c of each group of four, which spreads its
+// reads of values over the banks.
 __device__ __forceinline__ int row_token(int r) {
   const int c = (r & 7) >> 1;
   return (r & 8) + ((r & 1) ? 4 + (c ^ 1) : c);
@@ -229,29 +291,50 @@ __device__ __forceinline__ void write_row(const KvAttnArgs& a, const Item& it, i
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 2) k_kv_decode(const KvAttnArgs a, float* part) {
+__global__ void __launch_bounds__(kThreads, 2)
+    k_kv_decode(const KvAttnArgs a, float* part) {
   using C = Cfg<D, NT>;
-  constexpr int R = C::kRows, KS = D / 16, LD = D / 4;   // rows; reduction steps; values of a token in a lane
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int R = C::kRows, MT = D / 16;           // rows; 16-value tiles of the output
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int grp = warp >> 2, wq = warp & 3;          // group, and which 32 tokens of its tile
   Plan* plan = reinterpret_cast<Plan*>(smem + C::kOffPlan);
-  const uint32_t ring = smem_u32(smem) + warp * kStages * C::kStage;
-  const uint8_t* ringp = smem + warp * kStages * C::kStage;
-  const uint32_t bars = smem_u32(smem + C::kOffBar) + warp * kStages * 8;
   float* stat = reinterpret_cast<float*>(smem + C::kOffStat);
+  float* row_rs = reinterpret_cast<float*>(smem + C::kOffRow);
+  int *row_hi = reinterpret_cast<int*>(row_rs + R), *row_lo = row_hi + R;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffPlan - 16);
+  const uint32_t bar_s = sbase + C::kOffBar + 8 * grp;
+  const uint32_t off_k = sbase + grp * C::kGroup, off_v = off_k + kStagesK * C::kTile1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s)
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(bars + 8 * s) : "memory");
+  if (tid == 0) {
+    for (int b = 0; b < 2; ++b)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(sbase + C::kOffBar + 8 * b) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(tmem_slot)), "r"(C::kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
   make_plan<R>(a, blockIdx.x, gridDim.x, plan, reinterpret_cast<long long*>(smem + C::kOffPlan + 64), blockIdx.x == 0);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *tmem_slot;
+  if (grp == 0) {   // the digit sets' scales: 2^-6 and 2^6 everywhere
+    const uint32_t lo = 0x08080808u, hi = 0x68686868u;
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %1, %1, %1, %2, %2, %2, %2};"
+                 :: "r"(tmem + ((uint32_t)(32 * wq) << 16) + C::kColSFB), "r"(lo), "r"(hi) : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  }
   const long long first = plan->first, last = plan->total * (blockIdx.x + 1) / gridDim.x;
   int walk_b = plan->b;
   long long walk_at = plan->at;
-  uint32_t phases = 0;          // bit s: parity of the next wait on stage s
+  uint32_t ph_s = 0;            // parity of the next wait for scores
   bool dead = false;            // a wait gave up
-
   for (long long pos = first; pos < last;) {
     Item it;
     if (!find_item<R>(a, pos, walk_b, walk_at, it)) break;
@@ -260,237 +343,297 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_decode(const KvAttnArgs a, f
     const int ta = (int)(pos - it.start), tb = (int)min((long long)it.s.tiles, last - it.start);
     const long long seg_pos = pos;
     pos = it.start + tb;
-
-    // ---- copies of this warp's slice of tile k: page ids 32 tiles ahead, a lane each
     const int h = it.h;
-    const int32_t* row = a.pages + (long long)it.b * a.max_pages;
-    int ids = -1;
-    auto load_ids = [&](int k0) {
-      const int tok = it.s.base + (k0 + lane) * kTile + warp * kSlice;
-      ids = -1;
-      if (k0 + lane < tb && tok < it.s.hi) {
-        const int page = row[tok >> a.p.page_shift];
-        if (page >= 0 && page < a.p.num_pages) ids = page;
-        else if (a.status) atomicOr(a.status, FOS_STATUS_INDEX);
-      }
-    };
-    int issued = ta;             // next tile to issue
-    auto issue = [&]() {
-      if (((issued - ta) & 31) == 0) load_ids(issued);
-      const int page = __shfl_sync(~0u, ids, (issued - ta) & 31);
-      if (page >= 0 && lane == 0) {
-        const int st = (issued - ta) % kStages;
-        const int tok = it.s.base + issued * kTile + warp * kSlice;
-        const long long r = ((long long)h << a.p.page_shift) + (tok & ((1 << a.p.page_shift) - 1));
-        const long long co = page * a.p.codes_stride + r * (D / 2), so = page * a.p.scales_stride + r * (D / 16);
-        const uint32_t dst = ring + st * C::kStage, bar = bars + 8 * st;
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(C::kStage) : "memory");
-        bulk_load(dst, a.p.kc + co, C::kCodes, bar);
-        bulk_load(dst + C::kCodes, a.p.vc + co, C::kCodes, bar);
-        bulk_load(dst + 2 * C::kCodes, a.p.ks + so, C::kScales, bar);
-        bulk_load(dst + 2 * C::kCodes + C::kScales, a.p.vs + so, C::kScales, bar);
-      }
-      ++issued;
-      return page >= 0;
-    };
-    uint32_t flying = 0;         // bit s: stage s holds or awaits a slice
-    auto issue_next = [&]() {
-      const int st = (issued - ta) % kStages;
-      if (issue()) flying |= 1u << st;
-    };
-#pragma unroll 1
-    for (int i = 0; i < kStages - 1 && issued < tb; ++i) issue_next();
+    const int mine = (tb - ta + 1 - grp) / 2;          // this group's tiles: ta + grp + 2 i
+    const int32_t* ids_row = a.pages + (long long)it.b * a.max_pages;
+    auto token0 = [&](int i) { return it.s.base + (ta + grp + 2 * i) * kTile; };
 
-    // ---- queries: lane (g, c) holds values LD c .. LD c + LD - 1 of row g of each n-tile
-    uint32_t qf[NT][KS][2];
-    float rs[NT][2];             // scale of the scores of columns 2c, 2c + 1
-    int hi[NT][2], lo[NT][2];
-    int min_hi = 0x7fffffff, max_lo = 0;
+    // ---- a warp copies its own 32 tokens of a tile, 16 from one page at a
+    // time: the keys' codes into the swizzled operand, their scales into the
+    // atoms that go to tensor memory, the values as they are.  Page ids come
+    // 16 tiles at once, a lane for each 16 tokens, and one such window ahead.
+    auto load_ids = [&](int i0) {
+      const int i = i0 + (lane >> 1), tok = token0(i) + 32 * wq + kSlice * (lane & 1);
+      int page = -1;
+      if (i < mine && tok < it.s.hi) {
+        page = __ldg(ids_row + (tok >> a.p.page_shift));
+        if ((uint32_t)page >= (uint32_t)a.p.num_pages) {
+          page = -1;
+          if (a.status) atomicOr(a.status, FOS_STATUS_INDEX);
+        }
+      }
+      return page;
+    };
+    int ids = load_ids(0), ids_next = mine > 16 ? load_ids(16) : -1;
+    uint32_t copied = 0;         // which 16 tokens of tile i were copied: 2 bits at 2 (i mod 4)
+    const int in_page = (1 << a.p.page_shift) - 1;
+    auto issue = [&](int i, int sv) {
+      if ((i & 15) == 0 && i > 0) {
+        ids = ids_next;
+        ids_next = load_ids(i + 16);
+      }
+      const uint32_t dk = off_k + (i & 1) * C::kTile1, dv = off_v + sv * C::kTile1;
+      uint32_t live = 0;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int page = __shfl_sync(~0u, ids, 2 * (i & 15) + half);
+        if (page < 0) continue;
+        live |= 1u << half;
+        const int r = (h << a.p.page_shift) + ((token0(i) + 32 * wq + kSlice * half) & in_page);
+        const long long co = (long long)page * a.p.codes_stride + r * (D / 2) + lane * 16;
+        const long long so = (long long)page * a.p.scales_stride + r * (D / 16);
+        const int at = 32 * wq + kSlice * half;        // token of the tile
+        const int row = lane / (D / 32), chunk = lane & (D / 32 - 1);
+        const uint32_t k0 = dk + (at + row) * (D / 2) + ((chunk ^ row_chunk<D>(row)) << 4);
+        const uint32_t v0 = dv + at * (D / 2) + lane * 16;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) {             // 512 bytes of codes
+          copy16(k0 + 512 * e, a.p.kc + co + 512 * e);
+          copy16(v0 + 512 * e, a.p.vc + co + 512 * e);
+        }
+        // key scales: token t, 4 scales a word, word k at 512 k + 16 (t mod 32) + 4 (t / 32)
+        if (lane < 16 * (D / 64)) {
+          const int t = lane / (D / 64), k = lane & (D / 64 - 1);
+          copy4(dk + C::kCodes + 512 * k + (kSlice * half + t) * 16 + 4 * wq, a.p.ks + so + 4 * lane);
+        }
+        if (lane < D / 16) copy16(dv + C::kCodes + at * (D / 16) + 16 * lane, a.p.vs + so + 16 * lane);
+      }
+      copied = (copied & ~(3u << (2 * (i & 3)))) | live << (2 * (i & 3));
+    };
+    for (int i = 0; i < 2; ++i) {
+      if (i < mine) issue(i, i);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+
+    // ---- queries: a warp writes the digits of rows warp, warp + 8, ..
     const float base_scale = a.scale_log2 * a.p.kst[h];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = it.rt * R + 8 * nt + g;
-      float v[LD];
+    for (int rr = 0; rr < NT; ++rr) {
+      constexpr int E = D / 32;                          // values of a lane
+      const int r = warp + 8 * rr, row = it.rt * R + r;
+      const bool live = row < it.n * a.group;
+      float v[E];
 #pragma unroll
-      for (int k = 0; k < LD; ++k) v[k] = 0.0f;
-      if (r < it.n * a.group) {
-        const int i = r / a.group;
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)(it.q0 + i) * a.q_ld +
-                                                          (long long)(h * a.group + (r - i * a.group)) * D + LD * c);
+      for (int e = 0; e < E; ++e) v[e] = 0.0f;
+      if (live) {
+        const int i = row / a.group;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + (long long)(it.q0 + i) * a.q_ld +
+                                                                (long long)(h * a.group + (row - i * a.group)) * D) +
+                              lane * (E / 2);
 #pragma unroll
-        for (int k = 0; k < LD / 8; ++k) {
-          const uint4 w = __ldg(src + k);
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[8 * k + 2 * e] = bf_lo(x[e]);
-            v[8 * k + 2 * e + 1] = bf_hi(x[e]);
-          }
+        for (int e = 0; e < E / 2; ++e) {
+          const uint32_t w = __ldg(src + e);
+          v[2 * e] = bf_lo(w);
+          v[2 * e + 1] = bf_hi(w);
         }
       }
       uint32_t top = 0;          // |values| as bits: ordered like the values, NaN and Inf above all
 #pragma unroll
-      for (int k = 0; k < LD; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
-      top = max(top, __shfl_xor_sync(~0u, top, 1));
-      top = max(top, __shfl_xor_sync(~0u, top, 2));
-      const RowScale sc = row_scale(top);
-      const float mine = sc.finite ? base_scale * sc.down1 * sc.down2 : CUDART_NAN_F;
+      for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+      top = __reduce_max_sync(~0u, top);
+      const RowScale sc = row_scale(top);                // below 2^15; 2^8 more for the digits
+      uint32_t digits[8];
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+      for (int k = 0; k < 8; ++k) digits[k] = 0;
 #pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2)
-          qf[nt][k][e2] = sc.finite ? pack_h2(v[4 * k + 2 * e2] * sc.up1 * sc.up2, v[4 * k + 2 * e2 + 1] * sc.up1 * sc.up2)
-                                    : 0u;
+      for (int e = 0; e < E; ++e) {
+        int n = sc.finite ? __float2int_rn(v[e] * sc.up1 * sc.up2 * 256.0f) : 0;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        rs[nt][k] = __shfl_sync(~0u, mine, (2 * c + k) * 4);
-        const int rr = it.rt * R + 8 * nt + 2 * c + k;
-        hi[nt][k] = lo[nt][k] = 0;
-        if (rr < it.n * a.group) {
-          hi[nt][k] = query_hi(a, it.n, it.len, rr / a.group);
-          lo[nt][k] = query_lo(a, hi[nt][k]);
-          min_hi = min(min_hi, hi[nt][k]);
-          max_lo = max(max_lo, lo[nt][k]);
+        for (int k = 0; k < 8; ++k) {
+          const int d = k < 7 ? ((n + 4) & 7) - 4 : n;
+          n = (n - d) >> 3;
+          digits[k] |= (uint32_t)(d < 0 ? 8 - d : d) << (4 * e);
         }
       }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        uint8_t* dst = smem + C::kOffQ + (k >> 2) * C::kQ + row_at<D>((k & 3) * R + r, lane * (E / 2));
+        if (E == 4) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)digits[k];
+        else *dst = (uint8_t)digits[k];
+      }
+      if (lane == 0) {
+        const int hi = live ? query_hi(a, it.n, it.len, row / a.group) : 0;
+        // a digit is twice its E2M1 value, the low set's scale is 2^-6: 2^7; and the 2^8 from above
+        row_rs[r] = sc.finite ? base_scale * sc.down1 * sc.down2 * 0.5f : CUDART_NAN_F;
+        row_hi[r] = live ? hi : 0;
+        row_lo[r] = live ? query_lo(a, hi) : 0;
+      }
     }
-    // rows 2c, 2c + 1 over c cover all rows of the tile
-    min_hi = min(min_hi, __shfl_xor_sync(~0u, min_hi, 1));
-    min_hi = min(min_hi, __shfl_xor_sync(~0u, min_hi, 2));
-    max_lo = max(max_lo, __shfl_xor_sync(~0u, max_lo, 1));
-    max_lo = max(max_lo, __shfl_xor_sync(~0u, max_lo, 2));
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    int min_hi = 0x7fffffff, max_lo = 0;
+    {
+      const int r = lane & (R - 1);
+      if (it.rt * R + r < it.n * a.group) {
+        min_hi = row_hi[r];
+        max_lo = row_lo[r];
+      }
+      min_hi = __reduce_min_sync(~0u, min_hi);
+      max_lo = __reduce_max_sync(~0u, max_lo);
+    }
 
-    float m[NT][2], l[NT][2], acc[KS][NT][4];
+    // This thread's token is 32 wq + lane of the tile.  off = kLift - m, with m
+    // the maximum of a row, the same in all lanes; l: sums of this lane's tokens.
+    float2 rs[R / 2], off[R / 2], l[R / 2];
+    float acc[MT][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -CUDART_INF_F;
-      l[nt][0] = l[nt][1] = 0.0f;
+    for (int r = 0; r < R / 2; ++r) {
+      rs[r] = make_float2(row_rs[2 * r], row_rs[2 * r + 1]);
+      off[r] = make_float2(kLift - kNone, kLift - kNone);
+      l[r] = make_float2(0.0f, 0.0f);
+    }
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+    for (int k = 0; k < MT; ++k)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[k][nt][e] = 0.0f;
-    }
+
+    // ---- the scores of tile i into tensor memory
+    auto scores = [&](int i) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");     // all tiles' copies but the newest's
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      if (grp == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
+      else          asm volatile("bar.sync 2, 128;" ::: "memory");
+      if (wq == (i & 3) && lane == 0) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t sfa = tmem + C::kColSFA + 8 * grp, d = tmem + C::kCols * grp;
+        const uint32_t k0 = off_k + (i & 1) * C::kTile1;
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
+                       :: "r"(sfa + 4 * k), "l"(desc_sf(k0 + C::kCodes + 512 * k)) : "memory");
+#pragma unroll
+        for (int set = 0; set < 2; ++set)
+#pragma unroll
+          for (int k = 0; k < D / 64; ++k)
+            umma(d, desc_rows<D>(k0 + 32 * k), desc_rows<D>(sbase + C::kOffQ + set * C::kQ + 32 * k), C::kIdesc,
+                 sfa + 4 * k, tmem + C::kColSFB + 4 * set, set | k);
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                     :: "r"(bar_s) : "memory");
+      }
+      __syncwarp();
+    };
+    if (mine > 0) scores(0);
+    int sv = 0;                  // stage of this tile's values
 
 #pragma unroll 1
-    for (int k = ta; k < tb; ++k) {
-      if (issued < tb && !dead) issue_next();
-      const int st = (k - ta) % kStages;
-      if (!(flying & (1u << st))) continue;
-      flying &= ~(1u << st);
-      const uint32_t bar = bars + 8 * st, parity = (phases >> st) & 1;
-      if (!__all_sync(~0u, mbar_wait(bar, parity))) {
-        dead = true;             // give up, but let the copy land if it does
-        mbar_wait(bar, parity);
-      }
-      phases ^= 1u << st;
-      if (dead) continue;
-      const uint8_t* base = ringp + st * C::kStage;
-      const int tok0 = it.s.base + k * kTile + warp * kSlice;
-      const bool edge = tok0 + kSlice > min_hi || tok0 < max_lo;
+    for (int i = 0; i < mine; ++i) {
+      // After a wait that gave up a warp waits no more, but goes on to the group's barriers.
+      if (!dead && !__all_sync(~0u, mbar_wait(bar_s, ph_s))) dead = true;
+      ph_s ^= 1;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      uint32_t s[C::kCols];
+      tmem_ld(tmem + C::kCols * grp + ((uint32_t)(32 * wq) << 16), s);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      // the keys of tile i have been read, this warp's values of tile i - 1 too
+      if (i + 2 < mine) issue(i + 2, sv == 0 ? 2 : sv - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (i + 1 < mine) scores(i + 1);
 
-      // ---- scores
-      float s[NT][4];
+      // ---- softmax
+      const int tok0 = token0(i) + 32 * wq, tok = tok0 + lane;
+      const uint32_t live = copied >> (2 * (i & 3));
+      const bool edge = tok0 + 32 > min_hi || tok0 < max_lo || (live & 3u) != 3u;
+      const bool held = tok >= it.s.lo && tok < it.s.hi && ((live >> (lane >> 4)) & 1u);
+      float2 y[R / 2], x[R / 2];
+      float over = -CUDART_INF_F;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int r = 0; r < R / 2; ++r) {
+        auto col = [&](int j) {
+          return make_float2(__uint_as_float(s[j * R + 2 * r]), __uint_as_float(s[j * R + 2 * r + 1]));
+        };
+        const float2 e8 = make_float2(8.0f, 8.0f);
+        y[r] = fma2(fma2(fma2(col(3), e8, col(2)), e8, col(1)), e8, col(0));
+        x[r] = fma2(y[r], rs[r], off[r]);
+      }
+      if (edge) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
-      {
-        const int t0 = row_token(g), t1 = row_token(g + 8);
-        const uint8_t* ks = base + 2 * C::kCodes;
-        uint32_t w0[LD / 8], w1[LD / 8], s0[LD / 16], s1[LD / 16];
-        if (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(base + t0 * (D / 2) + 16 * c);
-          const uint4 y = *reinterpret_cast<const uint4*>(base + t1 * (D / 2) + 16 * c);
-          w0[0] = x.x; w0[1] = x.y; w0[LD / 8 - 2] = x.z; w0[LD / 8 - 1] = x.w;
-          w1[0] = y.x; w1[1] = y.y; w1[LD / 8 - 2] = y.z; w1[LD / 8 - 1] = y.w;
-          const uint32_t p = scales_h2(*reinterpret_cast<const uint16_t*>(ks + t0 * (D / 16) + 2 * c));
-          const uint32_t q = scales_h2(*reinterpret_cast<const uint16_t*>(ks + t1 * (D / 16) + 2 * c));
-          s0[0] = __byte_perm(p, 0u, 0x1010u); s0[LD / 16 - 1] = __byte_perm(p, 0u, 0x3232u);
-          s1[0] = __byte_perm(q, 0u, 0x1010u); s1[LD / 16 - 1] = __byte_perm(q, 0u, 0x3232u);
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(base + t0 * (D / 2) + 8 * c);
-          const uint2 y = *reinterpret_cast<const uint2*>(base + t1 * (D / 2) + 8 * c);
-          w0[0] = x.x; w0[1] = x.y;
-          w1[0] = y.x; w1[1] = y.y;
-          const uint32_t p = scales_h2(ks[t0 * (D / 16) + c] | (uint32_t)ks[t1 * (D / 16) + c] << 8);
-          s0[0] = __byte_perm(p, 0u, 0x1010u);
-          s1[0] = __byte_perm(p, 0u, 0x3232u);
+        for (int r = 0; r < R / 2; ++r) {
+          if (!held || tok >= row_hi[2 * r] || tok < row_lo[2 * r]) x[r].x = -CUDART_INF_F;
+          if (!held || tok >= row_hi[2 * r + 1] || tok < row_lo[2 * r + 1]) x[r].y = -CUDART_INF_F;
         }
+        // what lies outside the rows' tokens may be anything, NaN too: its scales become 0
+        if (!held) {
 #pragma unroll
-        for (int w = 0; w < LD / 8; ++w) {
-          const uint32_t a0 = hmul2(codes_h2<0>(w0[w]), s0[w >> 1]), a1 = hmul2(codes_h2<0>(w1[w]), s1[w >> 1]);
-          const uint32_t a2 = hmul2(codes_h2<1>(w0[w]), s0[w >> 1]), a3 = hmul2(codes_h2<1>(w1[w]), s1[w >> 1]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma(s[nt], a0, a1, a2, a3, qf[nt][2 * w][0], qf[nt][2 * w][1]);
-          const uint32_t b0 = hmul2(codes_h2<2>(w0[w]), s0[w >> 1]), b1 = hmul2(codes_h2<2>(w1[w]), s1[w >> 1]);
-          const uint32_t b2 = hmul2(codes_h2<3>(w0[w]), s0[w >> 1]), b3 = hmul2(codes_h2<3>(w1[w]), s1[w >> 1]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma(s[nt], b0, b1, b2, b3, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+          for (int k = 0; k < D / 64; ++k)
+            *reinterpret_cast<uint32_t*>(smem + (off_v - sbase) + sv * C::kTile1 + C::kCodes +
+                                         (32 * wq + lane) * (D / 16) + 4 * k) = 0;
         }
       }
-      // ---- softmax: entry e of s is token row g + 8 (e >> 1), column 2c + (e & 1)
-      bool raise = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int r = 0; r < R / 2; ++r) over = fmaxf(over, fmaxf(x[r].x, x[r].y));
+      if (__any_sync(~0u, over > kLift + kSlack)) {
+        float keep0[NT], keep1[NT];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[nt][e] *= rs[nt][e & 1];
-          if (edge) {
-            const int tok = tok0 + row_token(g + 8 * (e >> 1));
-            if (tok >= hi[nt][e & 1] || tok < lo[nt][e & 1]) s[nt][e] = -CUDART_INF_F;
-          }
-          raise |= s[nt][e] > m[nt][e & 1] + kSlack;
+        for (int r = 0; r < R; ++r) {
+          float& o = (r & 1) ? off[r / 2].y : off[r / 2].x;
+          float& lr = (r & 1) ? l[r / 2].y : l[r / 2].x;
+          float& xr = (r & 1) ? x[r / 2].y : x[r / 2].x;
+          const float rsr = (r & 1) ? rs[r / 2].y : rs[r / 2].x, yr = (r & 1) ? y[r / 2].y : y[r / 2].x;
+          const bool masked = xr == -CUDART_INF_F;
+          float t = masked ? kNone : yr * rsr;
+#pragma unroll
+          for (int o2 = 16; o2; o2 >>= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o2));
+          const float was = o, keep = kLift - t < was ? ex2(kLift - t - was) : 1.0f;
+          if (kLift - t < was) o = kLift - t;
+          lr *= keep;
+          if (!masked) xr = fmaf(yr, rsr, o);
+          if (2 * c == (r & 7)) keep0[r >> 3] = keep;
+          if (2 * c + 1 == (r & 7)) keep1[r >> 3] = keep;
         }
-      if (__any_sync(~0u, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            float t = fmaxf(s[nt][k2], s[nt][k2 + 2]);
-            t = fmaxf(t, __shfl_xor_sync(~0u, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
-            t = fmaxf(t, m[nt][k2]);
-            const float keep = t == m[nt][k2] ? 1.0f : ex2(m[nt][k2] - t);
-            m[nt][k2] = t;
-            l[nt][k2] *= keep;
-#pragma unroll
-            for (int i = 0; i < KS; ++i) {
-              acc[i][nt][k2] *= keep;
-              acc[i][nt][k2 + 2] *= keep;
-            }
+          for (int k = 0; k < MT; ++k) {
+            acc[k][nt][0] *= keep0[nt];
+            acc[k][nt][1] *= keep1[nt];
+            acc[k][nt][2] *= keep0[nt];
+            acc[k][nt][3] *= keep1[nt];
           }
       }
-      uint32_t pf[NT][2];
+      // the weights of 8 rows of a token are 16 bytes, [row tile][token]
+      uint8_t* pw = smem + C::kOffP + warp * 32 * R * 2;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float r0 = m[nt][0] == -CUDART_INF_F ? 0.0f : m[nt][0] - kLift;
-        const float r1 = m[nt][1] == -CUDART_INF_F ? 0.0f : m[nt][1] - kLift;
-        const float p0 = ex2(s[nt][0] - r0), p1 = ex2(s[nt][1] - r1), p2 = ex2(s[nt][2] - r0), p3 = ex2(s[nt][3] - r1);
-        l[nt][0] += p0 + p2;
-        l[nt][1] += p1 + p3;
-        pf[nt][0] = transpose8x8(pack_h2(p0, p1));
-        pf[nt][1] = transpose8x8(pack_h2(p2, p3));
+        uint32_t ph[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 p = make_float2(ex2(x[4 * nt + e].x), ex2(x[4 * nt + e].y));
+          l[4 * nt + e] = add2(l[4 * nt + e], p);
+          ph[e] = pack_h2(p.x, p.y);
+        }
+        *reinterpret_cast<uint4*>(pw + nt * 512 + lane * 16) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
       }
-      // ---- output
-      {
+      __syncwarp();
+
+      // ---- output (scores(i + 1), or the last tile's, waited for these values)
+      const uint8_t* vc = smem + (off_v - sbase) + sv * C::kTile1 + 32 * wq * (D / 2);
+      const uint8_t* vs = smem + (off_v - sbase) + sv * C::kTile1 + C::kCodes + 32 * wq * (D / 16);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t at = smem_u32(pw) + nt * 512 + (16 * half + row_token(lane & 15)) * 16;
+          asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+                       : "=r"(pf[nt][0]), "=r"(pf[nt][1]) : "r"(at) : "memory");
+        }
         constexpr int VW = D / 64;             // words of a token in a lane: 8 VW values from 8 VW g on
-        const uint8_t *vc = base + C::kCodes, *vs = base + 2 * C::kCodes + C::kScales;
         const int vb = (8 * VW * g) >> 4;      // their block
         uint32_t w[4][VW], sc[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int tok = row_token(2 * c + (t & 1) + 8 * (t >> 1));
+          const int vt = 16 * half + row_token(2 * c + (t & 1) + 8 * (t >> 1));
           if (VW == 2) {
-            const uint2 x = *reinterpret_cast<const uint2*>(vc + tok * (D / 2) + 8 * g);
-            w[t][0] = x.x;
-            w[t][VW - 1] = x.y;
+            const uint2 y = *reinterpret_cast<const uint2*>(vc + vt * (D / 2) + 8 * g);
+            w[t][0] = y.x;
+            w[t][VW - 1] = y.y;
           } else {
-            w[t][0] = *reinterpret_cast<const uint32_t*>(vc + tok * (D / 2) + 4 * g);
+            w[t][0] = *reinterpret_cast<const uint32_t*>(vc + vt * (D / 2) + 4 * g);
           }
-          sc[t] = vs[tok * (D / 16) + vb];
-          // what lies outside the rows' tokens may be anything, NaN too
-          if (edge && (tok0 + tok >= it.s.hi || tok0 + tok < it.s.lo)) sc[t] = 0;
+          sc[t] = vs[vt * (D / 16) + vb];
         }
         const uint32_t s01 = scales_h2(sc[0] | sc[1] << 8), s23 = scales_h2(sc[2] | sc[3] << 8);
 #pragma unroll
@@ -499,41 +642,44 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_decode(const KvAttnArgs a, f
           const uint32_t o01 = ((w[0][v] >> 4) & 0x0f0f0f0fu) | (w[1][v] & 0xf0f0f0f0u);
           const uint32_t e23 = (w[2][v] & 0x0f0f0f0fu) | ((w[3][v] << 4) & 0xf0f0f0f0u);
           const uint32_t o23 = ((w[2][v] >> 4) & 0x0f0f0f0fu) | (w[3][v] & 0xf0f0f0f0u);
-#define FOS_KV_PV(J)                                                                                              \
-  {                                                                                                               \
-    const uint32_t a0 = hmul2(codes_h2<J>(e01), s01), a1 = hmul2(codes_h2<J>(o01), s01);                          \
-    const uint32_t a2 = hmul2(codes_h2<J>(e23), s23), a3 = hmul2(codes_h2<J>(o23), s23);                          \
-    _Pragma("unroll") for (int nt = 0; nt < NT; ++nt) mma(acc[4 * v + J][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]); \
-  }
-          FOS_KV_PV(0)
-          FOS_KV_PV(1)
-          FOS_KV_PV(2)
-          FOS_KV_PV(3)
-#undef FOS_KV_PV
+          uint32_t he01[4], ho01[4], he23[4], ho23[4];
+          codes_h2x4(e01, he01);
+          codes_h2x4(o01, ho01);
+          codes_h2x4(e23, he23);
+          codes_h2x4(o23, ho23);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t a0 = hmul2(he01[q], s01), a1 = hmul2(ho01[q], s01);
+            const uint32_t a2 = hmul2(he23[q], s23), a3 = hmul2(ho23[q], s23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(acc[4 * v + q][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+          }
         }
       }
-      __syncwarp();              // all lanes are done with the stage before it is filled again
+      __syncwarp();              // the values' stage and the weights may be written again
+      sv = sv == 2 ? 0 : sv + 1;
     }
 
-    // ---- join the warps' results through shared memory (over the ring: its copies have all landed)
+    // ---- join the warps' results through shared memory (over the stages: their copies have all landed)
     __syncthreads();
     float* om = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float t = (r & 1) ? l[r / 2].y : l[r / 2].x;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+      if (lane == r) {
+        stat[warp * R + r] = kLift - ((r & 1) ? off[r / 2].y : off[r / 2].x);
+        stat[(kWarps + warp) * R + r] = t;
+      }
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int k2 = 0; k2 < 2; ++k2) {
-        float t = l[nt][k2];
-        t += __shfl_xor_sync(~0u, t, 4);
-        t += __shfl_xor_sync(~0u, t, 8);
-        t += __shfl_xor_sync(~0u, t, 16);
-        const int r = 8 * nt + 2 * c + k2;
-        if (g == 0) {
-          stat[warp * R + r] = m[nt][k2];
-          stat[(kWarps + warp) * R + r] = t;
-        }
-        float* dst = om + (warp * R + r) * C::kLdO + (D / 8) * g;
+        float* dst = om + (warp * R + 8 * nt + 2 * c + k2) * C::kLdO + (D / 8) * g;
 #pragma unroll
-        for (int i = 0; i < KS; ++i)
+        for (int i = 0; i < MT; ++i)
           *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][nt][k2], acc[i][nt][k2 + 2]);
       }
     __syncthreads();
@@ -562,10 +708,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_decode(const KvAttnArgs a, f
       }
     }
     __syncthreads();
-    // the ring was written by ordinary stores: order them before the next copies
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   if (dead && a.status) atomicOr(a.status, FOS_STATUS_TIMEOUT);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 0) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(C::kTmemCols) : "memory");
+  }
 }
 
 // Joins an item that several shares hold: the CTA of the share in which the

@@ -190,8 +190,9 @@ __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int thr
 
 // One 8-value word of codes times its block's scale -> 16 bytes
 __device__ __forceinline__ uint4 word_f16(uint32_t w, uint32_t s) {
-  return make_uint4(hmul2(codes_h2<0>(w), s), hmul2(codes_h2<1>(w), s), hmul2(codes_h2<2>(w), s),
-                    hmul2(codes_h2<3>(w), s));
+  uint32_t h[4];
+  codes_h2x4(w, h);
+  return make_uint4(hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
 }
 
 // The codes and scales of one token's head.
@@ -231,7 +232,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, float* part) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   const uint32_t sbase = smem_u32(smem), bar = sbase + C::kOffBar;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc);
   volatile uint32_t* fail = tmem_slot + 1;

@@ -19,6 +19,10 @@ a reduced batch so a capture stays small), runs one untimed call, then
   gemm      NVFP4 block-scaled GEMM, rows x rows x rows (rows a multiple of 256)
   linear    one step of the quantized Linear layer, 8192 x 4096 -> 4096: forward,
             dgrad and wgrad with x and dy quantized in the step (several kernels)
+  kv_append 8192 rotated tokens appended to a cache (32 query heads, 8 key/value heads of 128)
+  kv_read   their keys and values read back
+  kv_decode one query for each of 32 sequences of 8192 cached tokens
+  kv_prompt the attention of a prompt of `rows` tokens
 """
 from __future__ import annotations
 
@@ -108,6 +112,34 @@ def main():
         def fn():
             _, qx_t = F.linear_forward(xl, qw, save_colwise=True, seed=7)
             F.linear_backward(dyl, None, qw, seed=7, qx_t=qx_t)
+    elif c.startswith("kv_"):
+        n = {"kv_decode": 32 * 8192, "kv_prompt": args.rows}.get(c, 8192)
+        g = torch.Generator(device=dev).manual_seed(0)
+        cache = F.KVCache.empty(n // 64, 64, 8, 128, 5.0, 5.0, device=dev)
+        slots = torch.randperm(n // 64, generator=g, device=dev)[:, None] * 64 + torch.arange(64, device=dev)
+        slots = slots.flatten()
+        table = torch.ones(n, 128, device=dev) * 0.7071
+        pos = torch.arange(n, dtype=torch.int32, device=dev)
+
+        def some(heads, tokens):
+            return torch.randn(tokens, heads, 128, generator=g, device=dev).to(torch.bfloat16)
+
+        for i in range(0, n, 8192):
+            F.kv_append(cache, some(8, min(n, 8192)), some(8, min(n, 8192)), slots[i:i + 8192])
+        pages = (slots[::64] // 64).to(torch.int32)
+        if c == "kv_append":
+            q, k, v = some(32, n), some(8, n), some(8, n)
+            fn = lambda: F.kv_append(cache, k, v, slots, pos, table, q=q, q_out=q)
+        elif c == "kv_read":
+            out = F.kv_read(cache, slots)
+            fn = lambda: F.kv_read(cache, slots, out=out)
+        else:
+            b, each = (32, 1) if c == "kv_decode" else (1, n)
+            q = some(32, b * each)
+            cu = torch.arange(b + 1, dtype=torch.int32, device=dev) * each
+            kv_len = torch.full((b,), n // b, dtype=torch.int32, device=dev)
+            out = torch.empty_like(q)
+            fn = lambda: F.kv_attention(cache, q, cu, pages.view(b, -1), kv_len, each, out=out)
     else:
         raise SystemExit("unknown case " + c)
     fn()

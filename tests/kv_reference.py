@@ -46,10 +46,10 @@ def attention(q, kc, ks, vc, vs, kst, vst, cu, pages, kv_len, causal, window, sc
     """(out, lse, bound) in 64 bits for [total_q, Hq, D]; the bound is on
     |kernel - out| before and after its rounding to bf16.
 
-    With n keys, e = 2^-24 and every product exact: a score sums D products
-    (any order: D e times the sum of their magnitudes) and takes two more
-    roundings, so it is off by ds <= (D + 4) e |scale St| sum |q k|; its
-    exponential by 2 ds (score and maximum) + 2^-21 (exp2 and the reduced
+    With n keys, e = 2^-24: a score sums D products (any order: D e times the
+    sum of their magnitudes) and takes a few more roundings, and a query may
+    be held to 24 bits below its largest value, so a score is off by ds <=
+    e |scale St| ((D + 8) sum |q k| + max |q| sum |k|); its exponential by 2 ds (score and maximum) + 2^-21 (exp2 and the reduced
     argument); a weight is rounded to f16 (2^-11, or 2^-25 of the largest
     where it is subnormal); the sums over n keys add n e.  The result is
     rounded to bf16 (2^-8)."""
@@ -82,7 +82,8 @@ def attention(q, kc, ks, vc, vs, kst, vst, cu, pages, kv_len, causal, window, sc
                 t = cu[b] + i
                 out[t, h] = p @ v
                 lse[t, h] = top + np.log(total)
-                ds = ((D + 4) * 2.0 ** -24 * abs(scale) * (np.abs(k) @ np.abs(q[t, h]))).max()
+                ds = ((D + 8) * (np.abs(k) @ np.abs(q[t, h])) + np.abs(q[t, h]).max() * np.abs(k).sum(1)).max()
+                ds *= 2.0 ** -24 * abs(scale)
                 rel = 2 * ds + 2.0 ** -21 + (hi - lo) * 2.0 ** -23
                 mag = p @ np.abs(v)
                 bound[t, h] = (np.expm1(rel) + 2.0 ** -11) * mag * 1.01 + 2.0 ** -25 * np.abs(v).sum(0) / total

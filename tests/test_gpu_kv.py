@@ -413,3 +413,25 @@ def test_empty_calls():
     out, lse = F.kv_attention(cache, one, torch.tensor([0, 1], dtype=I32, device=dev),
                               torch.empty(1, 0, dtype=I32, device=dev), zero, 1, return_lse=True)
     assert not out.any() and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("max_q", [1, 200])
+def test_one_key_gives_its_values_for_every_code(dim, max_q):
+    """With a single visible key the answer is its values as kv_read gives
+    them, bit for bit: every byte of codes in every place of a row."""
+    dev = require_gpu()
+    n = 256
+    cache = F.KVCache.empty(n, 16, 2, dim, 3.0, 3.0, device=dev)
+    byte = torch.arange(n, device=dev)[:, None] + torch.arange(dim // 2, device=dev) * 37
+    for t in (cache.k_codes, cache.v_codes):
+        t.copy_((byte % 256).to(torch.uint8)[:, None, None])
+    for t in (cache.k_scales, cache.v_scales):
+        t.copy_((torch.arange(n, device=dev) % 0x7f).to(torch.uint8)[:, None, None, None])
+    slots = torch.arange(n, device=dev) * 16 + torch.arange(n, device=dev) % 16
+    pages = torch.arange(n, dtype=I32, device=dev)[:, None].contiguous()
+    kv_len = (torch.arange(n, device=dev) % 16 + 1).to(I32)
+    q = _queries(n, 4, dim, 60).to(dev)
+    got = F.kv_attention(cache, q, torch.arange(n + 1, dtype=I32, device=dev), pages, kv_len, max_q, window=1)
+    want = F.kv_read(cache, slots)[1].repeat_interleave(2, 1)
+    assert torch.equal(got, want)
