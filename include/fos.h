@@ -329,8 +329,8 @@ fos_status fos_quantize_static(const void* x, int64_t batch, int64_t rows, int64
  *   scales [num_pages][heads][page_size][head_dim / 16]  E4M3, one for each
  *          16 consecutive values of a token's head
  * A page is contiguous; pages are codes_page_stride and scales_page_stride
- * bytes apart (>= the page's size, multiples of 16), so one allocation may
- * hold the pools of several layers.  All pointers 16-byte aligned.
+ * bytes apart (>= the page's size, below 2^32, multiples of 16), so one
+ * allocation may hold the pools of several layers.  All pointers 16-byte aligned.
  *   k_tensor_scale, v_tensor_scale: float [heads], the FP32 scale S_t of each
  *          head, fixed before the first token is appended: A / (4 * 448) for
  *          4/6, A / (6 * 448) for 6-only, A the largest |value| expected.

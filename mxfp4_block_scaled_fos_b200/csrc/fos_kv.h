@@ -13,7 +13,9 @@ namespace fos {
 struct KvPool {
   uint8_t *kc, *ks, *vc, *vs;
   const float *kst, *vst;
-  long long codes_stride, scales_stride;  // between pages
+  long long codes_stride, scales_stride;  // between pages, below 2^32
+  uint32_t codes_stride32, scales_stride32;
+  long long kv_codes, kv_scales;          // from the keys' pools to the values'
   long long num_pages;
   int page_shift;                         // log2(page_size)
   int heads, dim;

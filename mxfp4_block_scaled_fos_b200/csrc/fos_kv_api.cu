@@ -22,6 +22,7 @@ fos_status check_pool(const fos_kv_cache* c, KvPool* p) {
   const int64_t rows = c->heads * c->page_size;
   if (c->codes_page_stride < rows * (c->head_dim / 2) || c->scales_page_stride < rows * (c->head_dim / 16))
     return FOS_ERR_SHAPE;
+  if (c->codes_page_stride > 0xffffffffll || c->scales_page_stride > 0xffffffffll) return FOS_ERR_SHAPE;
   if (c->codes_page_stride % 16 || c->scales_page_stride % 16) return FOS_ERR_ALIGN;
   if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) ||
       !aligned(c->v_scales, 16) || !aligned(c->k_tensor_scale, 4) || !aligned(c->v_tensor_scale, 4))
@@ -34,6 +35,10 @@ fos_status check_pool(const fos_kv_cache* c, KvPool* p) {
   p->vst = c->v_tensor_scale;
   p->codes_stride = c->codes_page_stride;
   p->scales_stride = c->scales_page_stride;
+  p->codes_stride32 = (uint32_t)c->codes_page_stride;
+  p->scales_stride32 = (uint32_t)c->scales_page_stride;
+  p->kv_codes = (long long)((uintptr_t)c->v_codes - (uintptr_t)c->k_codes);
+  p->kv_scales = (long long)((uintptr_t)c->v_scales - (uintptr_t)c->k_scales);
   p->num_pages = c->num_pages;
   p->page_shift = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
   p->heads = (int)c->heads;

@@ -62,8 +62,8 @@ struct Cfg {
   static constexpr int kOffP = kOffQ + 2 * kQ;                           // weights, [warp][32 tokens][rows] f16
   static constexpr int kOffStat = kOffP + kWarps * 32 * kRows * 2;       // m, l [warps][rows]
   static constexpr int kOffRow = kOffStat + 2 * kWarps * kRows * 4;      // rs, hi, lo [rows]
-  static constexpr int kOffBar = kOffRow + 3 * kRows * 4;                // a group's scores are there
-  static constexpr int kOffPlan = kOffBar + 2 * 8 + 16;
+  static constexpr int kOffBar = kOffRow + 3 * kRows * 4;                // of a group: scores done, keys ready
+  static constexpr int kOffPlan = kOffBar + 2 * 16 + 16;
   static constexpr int kSmem = kOffPlan + 64 + kWarps * 8 + 1024;        // + alignment slack
   static constexpr int kPart = kRows * (D + 2);                          // floats of one partial result
   static constexpr uint32_t kTmemCols = NT == 1 ? 128 : 256;
@@ -87,12 +87,34 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   return false;
 }
 
-// Copies straight to shared memory, 16 or 4 bytes.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Copies straight to shared memory, 16 or 4 bytes, where p.
+__device__ __forceinline__ void copy16(uint32_t dst, unsigned long long src, bool p) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "@p cp.async.cg.shared.global.L2::128B [%0], [%1], 16;\n\t}"
+      :: "r"(dst), "l"(src), "r"((uint32_t)p) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, unsigned long long src, bool p) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "@p cp.async.ca.shared.global [%0], [%1], 4;\n\t}"
+      :: "r"(dst), "l"(src), "r"((uint32_t)p) : "memory");
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -305,12 +327,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* row_rs = reinterpret_cast<float*>(smem + C::kOffRow);
   int *row_hi = reinterpret_cast<int*>(row_rs + R), *row_lo = row_hi + R;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffPlan - 16);
-  const uint32_t bar_s = sbase + C::kOffBar + 8 * grp;
+  const uint32_t bar_s = sbase + C::kOffBar + 16 * grp, bar_r = bar_s + 8;
   const uint32_t off_k = sbase + grp * C::kGroup, off_v = off_k + kStagesK * C::kTile1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
-    for (int b = 0; b < 2; ++b)
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(sbase + C::kOffBar + 8 * b) : "memory");
+    for (int b = 0; b < 4; ++b)   // scores: one commit; ready: an arrival from each warp of the group
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(sbase + C::kOffBar + 8 * b), "r"(b & 1 ? 4 : 1)
+                   : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -333,7 +356,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   const long long first = plan->first, last = plan->total * (blockIdx.x + 1) / gridDim.x;
   int walk_b = plan->b;
   long long walk_at = plan->at;
-  uint32_t ph_s = 0;            // parity of the next wait for scores
+  uint32_t ph_s = 0, ph_r = 0;  // parities of the next scores and of the next keys
+  // what a lane reads of a tile's values: tokens c, 4 + (c ^ 1) and both + 8, of 16 (row_token)
+  const uint32_t v_at0 = c * (D / 2) + (D / 16) * g, v_at1 = (4 + (c ^ 1)) * (D / 2) + (D / 16) * g;
+  const uint32_t vs_at0 = c * (D / 16) + g * D / 128, vs_at1 = (4 + (c ^ 1)) * (D / 16) + g * D / 128;
+  const uint32_t p_at = sbase + C::kOffP + warp * 32 * R * 2;   // this warp's weights
+  const uint32_t p_ld = p_at + row_token(lane & 15) * 16;
+  // where a lane's copies go in a tile: keys' codes (swizzled) and scales, values' codes and scales
+  const uint32_t k_at = (32 * wq + lane / (D / 32)) * (D / 2) +
+                        (((lane & (D / 32 - 1)) ^ row_chunk<D>(lane / (D / 32))) << 4);
+  const uint32_t ks_at = C::kCodes + 4 * wq + 512 * (lane & (D / 64 - 1)) + (lane / (D / 64)) * 16;
+  const uint32_t w_at = 32 * wq * (D / 2) + lane * 16, ws_at = C::kCodes + 32 * wq * (D / 16) + lane * 16;
   bool dead = false;            // a wait gave up
   for (long long pos = first; pos < last;) {
     Item it;
@@ -366,37 +399,34 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     int ids = load_ids(0), ids_next = mine > 16 ? load_ids(16) : -1;
     uint32_t copied = 0;         // which 16 tokens of tile i were copied: 2 bits at 2 (i mod 4)
-    const int in_page = (1 << a.p.page_shift) - 1;
+    const uint32_t in_page = (1u << a.p.page_shift) - 1;
+    // this head's part of page 0: a lane's bytes of the keys' codes and scales
+    const unsigned long long kc0 = (unsigned long long)a.p.kc + ((uint32_t)h << a.p.page_shift) * (D / 2) + lane * 16;
+    const unsigned long long ks0 = (unsigned long long)a.p.ks + ((uint32_t)h << a.p.page_shift) * (D / 16);
     auto issue = [&](int i, int sv) {
       if ((i & 15) == 0 && i > 0) {
         ids = ids_next;
         ids_next = load_ids(i + 16);
       }
       const uint32_t dk = off_k + (i & 1) * C::kTile1, dv = off_v + sv * C::kTile1;
+      const uint32_t tok = (uint32_t)token0(i) + 32 * wq;
       uint32_t live = 0;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int page = __shfl_sync(~0u, ids, 2 * (i & 15) + half);
-        if (page < 0) continue;
-        live |= 1u << half;
-        const int r = (h << a.p.page_shift) + ((token0(i) + 32 * wq + kSlice * half) & in_page);
-        const long long co = (long long)page * a.p.codes_stride + r * (D / 2) + lane * 16;
-        const long long so = (long long)page * a.p.scales_stride + r * (D / 16);
-        const int at = 32 * wq + kSlice * half;        // token of the tile
-        const int row = lane / (D / 32), chunk = lane & (D / 32 - 1);
-        const uint32_t k0 = dk + (at + row) * (D / 2) + ((chunk ^ row_chunk<D>(row)) << 4);
-        const uint32_t v0 = dv + at * (D / 2) + lane * 16;
+        const bool here = page >= 0;
+        if (here) live |= 1u << half;
+        const uint32_t r = (tok + kSlice * half) & in_page;
+        const unsigned long long kp = (unsigned long long)(uint32_t)page * a.p.codes_stride32 + (kc0 + r * (D / 2));
+        const unsigned long long sp = (unsigned long long)(uint32_t)page * a.p.scales_stride32 + (ks0 + r * (D / 16));
 #pragma unroll
-        for (int e = 0; e < D / 64; ++e) {             // 512 bytes of codes
-          copy16(k0 + 512 * e, a.p.kc + co + 512 * e);
-          copy16(v0 + 512 * e, a.p.vc + co + 512 * e);
+        for (int e = 0; e < D / 64; ++e) {             // 16 tokens: 512 bytes at a time
+          copy16(dk + k_at + kSlice * half * (D / 2) + 512 * e, kp + 512 * e, here);
+          copy16(dv + w_at + kSlice * half * (D / 2) + 512 * e, kp + a.p.kv_codes + 512 * e, here);
         }
         // key scales: token t, 4 scales a word, word k at 512 k + 16 (t mod 32) + 4 (t / 32)
-        if (lane < 16 * (D / 64)) {
-          const int t = lane / (D / 64), k = lane & (D / 64 - 1);
-          copy4(dk + C::kCodes + 512 * k + (kSlice * half + t) * 16 + 4 * wq, a.p.ks + so + 4 * lane);
-        }
-        if (lane < D / 16) copy16(dv + C::kCodes + at * (D / 16) + 16 * lane, a.p.vs + so + 16 * lane);
+        copy4(dk + ks_at + kSlice * half * 16, sp + 4 * lane, here && lane < 16 * (D / 64));
+        copy16(dv + ws_at + kSlice * half * (D / 16), sp + a.p.kv_scales + 16 * lane, here && lane < D / 16);
       }
       copied = (copied & ~(3u << (2 * (i & 3)))) | live << (2 * (i & 3));
     };
@@ -489,56 +519,59 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[k][nt][e] = 0.0f;
 
-    // ---- the scores of tile i into tensor memory
-    auto scores = [&](int i) {
+    // ---- the scores of tile i into tensor memory: every warp says when its
+    // keys have landed and the scores before them have been read; warp i mod 4
+    // waits for that and issues the products
+    auto ready = [&]() {
       asm volatile("cp.async.wait_group 1;" ::: "memory");     // all tiles' copies but the newest's
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      if (grp == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
-      else          asm volatile("bar.sync 2, 128;" ::: "memory");
-      if (wq == (i & 3) && lane == 0) {
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t sfa = tmem + C::kColSFA + 8 * grp, d = tmem + C::kCols * grp;
-        const uint32_t k0 = off_k + (i & 1) * C::kTile1;
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k)
-          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
-                       :: "r"(sfa + 4 * k), "l"(desc_sf(k0 + C::kCodes + 512 * k)) : "memory");
-#pragma unroll
-        for (int set = 0; set < 2; ++set)
+      __syncwarp();
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0;\n\t"
+          "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}"
+          :: "r"(bar_r), "r"(lane) : "memory");
+    };
+    auto scores = [&](int i) {
+      if (wq == (i & 3)) {
+        if (!dead && !__all_sync(~0u, mbar_wait(bar_r, ph_r))) dead = true;
+        if (lane == 0) {
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t sfa = tmem + C::kColSFA + 8 * grp, d = tmem + C::kCols * grp;
+          const uint32_t k0 = off_k + (i & 1) * C::kTile1;
 #pragma unroll
           for (int k = 0; k < D / 64; ++k)
-            umma(d, desc_rows<D>(k0 + 32 * k), desc_rows<D>(sbase + C::kOffQ + set * C::kQ + 32 * k), C::kIdesc,
-                 sfa + 4 * k, tmem + C::kColSFB + 4 * set, set | k);
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                     :: "r"(bar_s) : "memory");
+            asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
+                         :: "r"(sfa + 4 * k), "l"(desc_sf(k0 + C::kCodes + 512 * k)) : "memory");
+#pragma unroll
+          for (int set = 0; set < 2; ++set)
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k)
+              umma(d, desc_rows<D>(k0 + 32 * k), desc_rows<D>(sbase + C::kOffQ + set * C::kQ + 32 * k), C::kIdesc,
+                   sfa + 4 * k, tmem + C::kColSFB + 4 * set, set | k);
+          asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                       :: "r"(bar_s) : "memory");
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      ph_r ^= 1;
     };
-    if (mine > 0) scores(0);
+    if (mine > 0) {
+      ready();
+      scores(0);
+    }
     int sv = 0;                  // stage of this tile's values
 
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
-      // After a wait that gave up a warp waits no more, but goes on to the group's barriers.
+      // after a wait that gave up a warp waits no more
       if (!dead && !__all_sync(~0u, mbar_wait(bar_s, ph_s))) dead = true;
       ph_s ^= 1;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       uint32_t s[C::kCols];
       tmem_ld(tmem + C::kCols * grp + ((uint32_t)(32 * wq) << 16), s);
       asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-      // the keys of tile i have been read, this warp's values of tile i - 1 too
-      if (i + 2 < mine) issue(i + 2, sv == 0 ? 2 : sv - 1);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (i + 1 < mine) scores(i + 1);
-
-      // ---- softmax
-      const int tok0 = token0(i) + 32 * wq, tok = tok0 + lane;
-      const uint32_t live = copied >> (2 * (i & 3));
-      const bool edge = tok0 + 32 > min_hi || tok0 < max_lo || (live & 3u) != 3u;
-      const bool held = tok >= it.s.lo && tok < it.s.hi && ((live >> (lane >> 4)) & 1u);
-      float2 y[R / 2], x[R / 2];
-      float over = -CUDART_INF_F;
+      float2 y[R / 2];           // the scores, before their row's scale
 #pragma unroll
       for (int r = 0; r < R / 2; ++r) {
         auto col = [&](int j) {
@@ -546,9 +579,24 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         const float2 e8 = make_float2(8.0f, 8.0f);
         y[r] = fma2(fma2(fma2(col(3), e8, col(2)), e8, col(1)), e8, col(0));
-        x[r] = fma2(y[r], rs[r], off[r]);
       }
+      // the keys of tile i have been read, this warp's values of tile i - 1 too
+      if (i + 2 < mine) issue(i + 2, sv == 0 ? 2 : sv - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (i + 1 < mine) ready();
+
+      // ---- softmax
+      const int tok0 = token0(i) + 32 * wq;
+      const uint32_t live = copied >> (2 * (i & 3));
+      const bool edge = tok0 + 32 > min_hi || tok0 < max_lo || (live & 3u) != 3u;
+      float2 x[R / 2];
+      float over = -CUDART_INF_F;
+#pragma unroll
+      for (int r = 0; r < R / 2; ++r) x[r] = fma2(y[r], rs[r], off[r]);
       if (edge) {
+        __syncwarp();            // a branch, not predicates: few tiles come here
+        const int tok = tok0 + lane;
+        const bool held = tok >= it.s.lo && tok < it.s.hi && ((live >> (lane >> 4)) & 1u);
 #pragma unroll
         for (int r = 0; r < R / 2; ++r) {
           if (!held || tok >= row_hi[2 * r] || tok < row_lo[2 * r]) x[r].x = -CUDART_INF_F;
@@ -594,7 +642,6 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
       }
       // the weights of 8 rows of a token are 16 bytes, [row tile][token]
-      uint8_t* pw = smem + C::kOffP + warp * 32 * R * 2;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         uint32_t ph[4];
@@ -604,36 +651,35 @@ __global__ void __launch_bounds__(kThreads, 2)
           l[4 * nt + e] = add2(l[4 * nt + e], p);
           ph[e] = pack_h2(p.x, p.y);
         }
-        *reinterpret_cast<uint4*>(pw + nt * 512 + lane * 16) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(p_at + nt * 512 + lane * 16), "r"(ph[0]), "r"(ph[1]), "r"(ph[2]), "r"(ph[3]) : "memory");
       }
       __syncwarp();
 
-      // ---- output (scores(i + 1), or the last tile's, waited for these values)
-      const uint8_t* vc = smem + (off_v - sbase) + sv * C::kTile1 + 32 * wq * (D / 2);
-      const uint8_t* vs = smem + (off_v - sbase) + sv * C::kTile1 + C::kCodes + 32 * wq * (D / 16);
+      // ---- output (the wait for this tile's keys was one for its values too)
+      const uint32_t vbase = off_v + sv * C::kTile1 + 32 * wq * (D / 2);
+      const uint32_t sbase_v = off_v + sv * C::kTile1 + C::kCodes + 32 * wq * (D / 16);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        if (half == 1 && i + 1 < mine) scores(i + 1);   // by now the other warps are ready as a rule
         uint32_t pf[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint32_t at = smem_u32(pw) + nt * 512 + (16 * half + row_token(lane & 15)) * 16;
+        for (int nt = 0; nt < NT; ++nt)
           asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
-                       : "=r"(pf[nt][0]), "=r"(pf[nt][1]) : "r"(at) : "memory");
-        }
+                       : "=r"(pf[nt][0]), "=r"(pf[nt][1]) : "r"(p_ld + nt * 512 + 256 * half) : "memory");
         constexpr int VW = D / 64;             // words of a token in a lane: 8 VW values from 8 VW g on
-        const int vb = (8 * VW * g) >> 4;      // their block
         uint32_t w[4][VW], sc[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int vt = 16 * half + row_token(2 * c + (t & 1) + 8 * (t >> 1));
+          const uint32_t at = (t & 1 ? v_at1 : v_at0) + vbase + (16 * half + 8 * (t >> 1)) * (D / 2);
           if (VW == 2) {
-            const uint2 y = *reinterpret_cast<const uint2*>(vc + vt * (D / 2) + 8 * g);
+            const uint2 y = lds64(at);
             w[t][0] = y.x;
             w[t][VW - 1] = y.y;
           } else {
-            w[t][0] = *reinterpret_cast<const uint32_t*>(vc + vt * (D / 2) + 4 * g);
+            w[t][0] = lds32(at);
           }
-          sc[t] = vs[vt * (D / 16) + vb];
+          sc[t] = lds8((t & 1 ? vs_at1 : vs_at0) + sbase_v + (16 * half + 8 * (t >> 1)) * (D / 16));
         }
         const uint32_t s01 = scales_h2(sc[0] | sc[1] << 8), s23 = scales_h2(sc[2] | sc[3] << 8);
 #pragma unroll

@@ -21,7 +21,7 @@ a reduced batch so a capture stays small), runs one untimed call, then
             dgrad and wgrad with x and dy quantized in the step (several kernels)
   kv_append 8192 rotated tokens appended to a cache (32 query heads, 8 key/value heads of 128)
   kv_read   their keys and values read back
-  kv_decode one query for each of 32 sequences of 8192 cached tokens
+  kv_decode one query for each of 4 * experts sequences over 262144 cached tokens in all
   kv_prompt the attention of a prompt of `rows` tokens
 """
 from __future__ import annotations
@@ -134,7 +134,7 @@ def main():
             out = F.kv_read(cache, slots)
             fn = lambda: F.kv_read(cache, slots, out=out)
         else:
-            b, each = (32, 1) if c == "kv_decode" else (1, n)
+            b, each = (args.experts * 4, 1) if c == "kv_decode" else (1, n)
             q = some(32, b * each)
             cu = torch.arange(b + 1, dtype=torch.int32, device=dev) * each
             kv_len = torch.full((b,), n // b, dtype=torch.int32, device=dev)

@@ -29,7 +29,7 @@ def _cache(**kw):
 BAD_POOLS = [
     (dict(k_codes=None), NULL), (dict(v_tensor_scale=None), NULL), (dict(v_scales=136), ALIGN),
     (dict(k_codes=72), ALIGN), (dict(k_tensor_scale=322), ALIGN), (dict(codes_page_stride=1000), SHAPE),
-    (dict(codes_page_stride=1032), ALIGN), (dict(scales_page_stride=64), SHAPE), (dict(scales_page_stride=136), ALIGN),
+    (dict(codes_page_stride=1032), ALIGN), (dict(codes_page_stride=1 << 32), SHAPE), (dict(scales_page_stride=64), SHAPE), (dict(scales_page_stride=136), ALIGN),
     (dict(head_dim=80), UNSUPPORTED), (dict(head_dim=256), UNSUPPORTED), (dict(page_size=24), UNSUPPORTED),
     (dict(page_size=8), UNSUPPORTED), (dict(heads=0), SHAPE), (dict(num_pages=-1), SHAPE), (dict(num_pages=1 << 31), SHAPE),
 ]
