@@ -51,6 +51,7 @@ constexpr uint32_t kWaitLimit = 1u << 20;
 template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;                          // on an SM: 16 rows take all registers
   static constexpr int kCols = 4 * kRows;                                // score columns: row r, digits j: j * kRows + r
   static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16; // bytes of a tile's keys (or values)
   static constexpr int kTile1 = kCodes + kScales;
@@ -103,18 +104,20 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   return v;
 }
 
-// Copies straight to shared memory, 16 or 4 bytes, where p.
-__device__ __forceinline__ void copy16(uint32_t dst, unsigned long long src, bool p) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
-      "@p cp.async.cg.shared.global.L2::128B [%0], [%1], 16;\n\t}"
-      :: "r"(dst), "l"(src), "r"((uint32_t)p) : "memory");
+// Copies straight to shared memory: 16 bytes, or 4, of which n are read and
+// the others written as zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, unsigned long long src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, unsigned long long src, bool p) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
-      "@p cp.async.ca.shared.global [%0], [%1], 4;\n\t}"
-      :: "r"(dst), "l"(src), "r"((uint32_t)p) : "memory");
+__device__ __forceinline__ void copy4(uint32_t dst, unsigned long long src, uint32_t n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// m ? a : b, bit by bit
+__device__ __forceinline__ uint32_t select_bits(uint32_t m, uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xca;" : "=r"(d) : "r"(m), "r"(a), "r"(b));
+  return d;
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -212,6 +215,22 @@ struct Plan {
   int b;
 };
 
+// Share s of `shares` begins at tile s * base + min(s, rest).
+struct Split {
+  long long base;
+  int rest;
+  __device__ __forceinline__ Split(long long total, int shares) {
+    base = total / shares;
+    rest = (int)(total - base * shares);
+  }
+  __device__ __forceinline__ long long first(int s) const { return base * s + min(s, rest); }
+  // the share that holds tile x
+  __device__ __forceinline__ int of(long long x) const {
+    const long long big = (base + 1) * rest;
+    return x < big ? (int)(x / (base + 1)) : rest + (int)((x - big) / base);
+  }
+};
+
 // Every thread of the block takes part.  plan.b = batch when the share is empty.
 template <int ROWS>
 __device__ __forceinline__ void make_plan(const KvAttnArgs& a, int share, int shares, Plan* plan, long long* warp_sum,
@@ -243,7 +262,7 @@ __device__ __forceinline__ void make_plan(const KvAttnArgs& a, int share, int sh
     total += warp_sum[w];
   }
   upto += before;
-  const long long first = total * share / shares;
+  const long long first = Split(total, shares).first(share);
   if (tid == 0) { plan->total = total; plan->first = first; }
   if (first >= upto - mine && first < upto) {
     long long at = upto - mine;
@@ -313,7 +332,7 @@ __device__ __forceinline__ void write_row(const KvAttnArgs& a, const Item& it, i
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     k_kv_decode(const KvAttnArgs a, float* part) {
   using C = Cfg<D, NT>;
   constexpr int R = C::kRows, MT = D / 16;           // rows; 16-value tiles of the output
@@ -353,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   }
-  const long long first = plan->first, last = plan->total * (blockIdx.x + 1) / gridDim.x;
+  const long long first = plan->first, last = Split(plan->total, gridDim.x).first(blockIdx.x + 1);
   int walk_b = plan->b;
   long long walk_at = plan->at;
   uint32_t ph_s = 0, ph_r = 0;  // parities of the next scores and of the next keys
@@ -398,42 +417,47 @@ __global__ void __launch_bounds__(kThreads, 2)
       return page;
     };
     int ids = load_ids(0), ids_next = mine > 16 ? load_ids(16) : -1;
-    uint32_t copied = 0;         // which 16 tokens of tile i were copied: 2 bits at 2 (i mod 4)
     const uint32_t in_page = (1u << a.p.page_shift) - 1;
-    // this head's part of page 0: a lane's bytes of the keys' codes and scales
+    // this head's part of page 0: a lane's bytes of the keys' codes, the keys' scales
     const unsigned long long kc0 = (unsigned long long)a.p.kc + ((uint32_t)h << a.p.page_shift) * (D / 2) + lane * 16;
     const unsigned long long ks0 = (unsigned long long)a.p.ks + ((uint32_t)h << a.p.page_shift) * (D / 16);
-    auto issue = [&](int i, int sv) {
-      if ((i & 15) == 0 && i > 0) {
-        ids = ids_next;
-        ids_next = load_ids(i + 16);
-      }
-      const uint32_t dk = off_k + (i & 1) * C::kTile1, dv = off_v + sv * C::kTile1;
-      const uint32_t tok = (uint32_t)token0(i) + 32 * wq;
-      uint32_t live = 0;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int page = __shfl_sync(~0u, ids, 2 * (i & 15) + half);
-        const bool here = page >= 0;
-        if (here) live |= 1u << half;
-        const uint32_t r = (tok + kSlice * half) & in_page;
-        const unsigned long long kp = (unsigned long long)(uint32_t)page * a.p.codes_stride32 + (kc0 + r * (D / 2));
-        const unsigned long long sp = (unsigned long long)(uint32_t)page * a.p.scales_stride32 + (ks0 + r * (D / 16));
-#pragma unroll
-        for (int e = 0; e < D / 64; ++e) {             // 16 tokens: 512 bytes at a time
-          copy16(dk + k_at + kSlice * half * (D / 2) + 512 * e, kp + 512 * e, here);
-          copy16(dv + w_at + kSlice * half * (D / 2) + 512 * e, kp + a.p.kv_codes + 512 * e, here);
+    // The next tile to copy, its 32 tokens' first, and where it goes; which 16
+    // tokens of it (bits 0, 1) and of the tiles before it were copied.
+    uint32_t copy_tok = (uint32_t)token0(0) + 32 * wq, copy_k = off_k, copy_v = off_v, copied = 0;
+    int copy_i = 0;
+    auto issue = [&]() {
+      copied <<= 2;
+      if (copy_i < mine) {
+        if ((copy_i & 15) == 0 && copy_i > 0) {
+          ids = ids_next;
+          ids_next = load_ids(copy_i + 16);
         }
-        // key scales: token t, 4 scales a word, word k at 512 k + 16 (t mod 32) + 4 (t / 32)
-        copy4(dk + ks_at + kSlice * half * 16, sp + 4 * lane, here && lane < 16 * (D / 64));
-        copy16(dv + ws_at + kSlice * half * (D / 16), sp + a.p.kv_scales + 16 * lane, here && lane < D / 16);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int page = __shfl_sync(~0u, ids, (2 * copy_i & 30) + half);
+          const uint32_t n = page >= 0 ? 16u : 0u, p = (uint32_t)max(page, 0);
+          copied |= (n >> 4) << half;
+          const uint32_t r = (copy_tok + kSlice * half) & in_page;
+          const unsigned long long kp = (unsigned long long)p * a.p.codes_stride32 + (kc0 + r * (D / 2));
+          const unsigned long long sp = (unsigned long long)p * a.p.scales_stride32 + (ks0 + r * (D / 16));
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e) {           // 16 tokens: 512 bytes at a time
+            copy16(copy_k + k_at + kSlice * half * (D / 2) + 512 * e, kp + 512 * e, n);
+            copy16(copy_v + w_at + kSlice * half * (D / 2) + 512 * e, kp + a.p.kv_codes + 512 * e, n);
+          }
+          // key scales: token t, 4 scales a word, word k at 512 k + 16 (t mod 32) + 4 (t / 32)
+          if (D == 128 || lane < 16) copy4(copy_k + ks_at + kSlice * half * 16, sp + 4 * lane, n >> 2);
+          if (lane < D / 16) copy16(copy_v + ws_at + kSlice * half * (D / 16), sp + a.p.kv_scales + 16 * lane, n);
+        }
+        copy_tok += 2 * kTile;
+        copy_k = 2 * off_k + C::kTile1 - copy_k;
+        copy_v = copy_v == off_v + 2 * C::kTile1 ? off_v : copy_v + C::kTile1;
+        ++copy_i;
       }
-      copied = (copied & ~(3u << (2 * (i & 3)))) | live << (2 * (i & 3));
-    };
-    for (int i = 0; i < 2; ++i) {
-      if (i < mine) issue(i, i);
       asm volatile("cp.async.commit_group;" ::: "memory");
-    }
+    };
+    issue();
+    issue();
 
     // ---- queries: a warp writes the digits of rows warp, warp + 8, ..
     const float base_scale = a.scale_log2 * a.p.kst[h];
@@ -581,13 +605,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         y[r] = fma2(fma2(fma2(col(3), e8, col(2)), e8, col(1)), e8, col(0));
       }
       // the keys of tile i have been read, this warp's values of tile i - 1 too
-      if (i + 2 < mine) issue(i + 2, sv == 0 ? 2 : sv - 1);
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      issue();
       if (i + 1 < mine) ready();
 
       // ---- softmax
       const int tok0 = token0(i) + 32 * wq;
-      const uint32_t live = copied >> (2 * (i & 3));
+      const uint32_t live = copied >> 4;       // two tiles were issued after this one
       const bool edge = tok0 + 32 > min_hi || tok0 < max_lo || (live & 3u) != 3u;
       float2 x[R / 2];
       float over = -CUDART_INF_F;
@@ -684,10 +707,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t s01 = scales_h2(sc[0] | sc[1] << 8), s23 = scales_h2(sc[2] | sc[3] << 8);
 #pragma unroll
         for (int v = 0; v < VW; ++v) {
-          const uint32_t e01 = (w[0][v] & 0x0f0f0f0fu) | ((w[1][v] << 4) & 0xf0f0f0f0u);
-          const uint32_t o01 = ((w[0][v] >> 4) & 0x0f0f0f0fu) | (w[1][v] & 0xf0f0f0f0u);
-          const uint32_t e23 = (w[2][v] & 0x0f0f0f0fu) | ((w[3][v] << 4) & 0xf0f0f0f0u);
-          const uint32_t o23 = ((w[2][v] >> 4) & 0x0f0f0f0fu) | (w[3][v] & 0xf0f0f0f0u);
+          const uint32_t e01 = select_bits(0x0f0f0f0fu, w[0][v], w[1][v] << 4);
+          const uint32_t o01 = select_bits(0x0f0f0f0fu, w[0][v] >> 4, w[1][v]);
+          const uint32_t e23 = select_bits(0x0f0f0f0fu, w[2][v], w[3][v] << 4);
+          const uint32_t o23 = select_bits(0x0f0f0f0fu, w[2][v] >> 4, w[3][v]);
           uint32_t he01[4], ho01[4], he23[4], ho23[4];
           codes_h2x4(e01, he01);
           codes_h2x4(o01, ho01);
@@ -773,31 +796,29 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttnArgs a, const 
   __shared__ Plan plan;
   __shared__ long long sums[kWarps];
   make_plan<R>(a, blockIdx.x, gridDim.x, &plan, sums, false);
-  const long long total = plan.total, first = plan.first, last = total * (blockIdx.x + 1) / gridDim.x;
+  const Split split(plan.total, gridDim.x);
+  const long long first = plan.first, last = split.first(blockIdx.x + 1);
   Item it;
   const bool mine = first < last && find_item<R>(a, first, plan.b, plan.at, it) && first > it.start &&
                     it.start + it.s.tiles <= last;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!mine) return;
-  // the share that holds the item's first tile: the last one that begins at or before it
-  int c0 = (int)(it.start * gridDim.x / total);
-  while (c0 + 1 < (int)gridDim.x && total * (c0 + 1) / gridDim.x <= it.start) ++c0;
-  while (c0 > 0 && total * c0 / gridDim.x > it.start) --c0;
+  // the item is the first segment of every share but the one that it begins inside
+  const int c0 = split.of(it.start), n = blockIdx.x - c0 + 1;
+  const float* p0 = part + (long long)(2 * c0 + (split.first(c0) < it.start ? 1 : 0)) * C::kPart;
+  const float* p1 = part + (long long)(2 * c0) * C::kPart;
   for (int x = threadIdx.x; x < R * (D / 4); x += kThreads) {
     const int r = x / (D / 4), d = (x - r * (D / 4)) * 4;
     if (it.rt * R + r >= it.n * a.group) continue;
     float M = -CUDART_INF_F, L = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = c0; s <= (int)blockIdx.x; ++s) {
-      // a share that holds nothing is passed over; the item is the first segment
-      // of every share but the one that it begins inside
-      const long long f0 = total * s / gridDim.x, f1 = total * (s + 1) / gridDim.x;
-      if (f0 == f1) continue;
-      const float* p = part + (long long)(2 * s + (s == c0 && f0 < it.start ? 1 : 0)) * C::kPart;
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float* p = s ? p1 + (long long)(2 * s) * C::kPart : p0;
       const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
-      const float pm = p[R * D + r], top = fmaxf(M, pm);
+      const float pm = p[R * D + r], pl = p[R * D + R + r], top = fmaxf(M, pm);
       const float f = M == top ? 1.0f : ex2(M - top), k = pm == top ? 1.0f : ex2(pm - top);
-      L = L * f + p[R * D + R + r] * k;
+      L = L * f + pl * k;
       o.x = o.x * f + v.x * k; o.y = o.y * f + v.y * k; o.z = o.z * f + v.z * k; o.w = o.w * f + v.w * k;
       M = top;
     }
@@ -815,7 +836,7 @@ cudaError_t launch(const KvAttnArgs& a, float* part, cudaStream_t st) {
       (e = cudaFuncSetAttribute(k_kv_decode<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) !=
           cudaSuccess)
     return e;
-  const int ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+  const int ctas = C::kCtas * sms < kMaxCtas ? C::kCtas * sms : kMaxCtas;
   k_kv_decode<D, NT><<<ctas, kThreads, C::kSmem, st>>>(a, part);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // a table of one tile at most: no item is ever shared

@@ -101,6 +101,7 @@ class KVCache:
                           k_tensor_scale.data_ptr(), v_tensor_scale.data_ptr(), n, p, h, 2 * half,
                           k_codes.stride(0), k_scales.stride(0))
         self._ref = ctypes.byref(self._c)
+        self._dev, self._fmt, self._scale = k_codes.get_device(), fos.FMT[fmt], 1.0 / math.sqrt(2 * half)
 
     @classmethod
     def empty(cls, pages: int, page_size: int, heads: int, head_dim: int, k_amax: Union[float, torch.Tensor],
@@ -118,49 +119,52 @@ class KVCache:
         return cls(*pools, *st, fmt=fmt)
 
 
-class _on:
-    """The tensors' device as the current one, and the stream to use on it."""
-
-    def __init__(self, dev, stream):
-        self._guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-        self._dev, self._stream = dev, stream
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        s = self._stream if self._stream is not None else torch.cuda.current_stream(self._dev)
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+# The device of the tensors as the current one (left as it was), and the raw
+# handle of the stream to use on it.  Decoding steps launch a few microseconds
+# of work a call, so the usual case asks for nothing but two integers.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(name: str, x: torch.Tensor, tokens: int, heads: Optional[int], cache: KVCache) -> None:
-    if x.dtype != torch.bfloat16 or x.device != cache.device:
+def _call(cache: "KVCache", what: str, fn, stream, args) -> None:
+    dev = cache._dev
+    s = _current_stream(dev) if stream is None else stream.cuda_stream
+    if _current_device() == dev:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st != 0:
+        raise fos.FosError(st, what)
+
+
+def _rows(name: str, x: torch.Tensor, tokens: int, heads: int, cache: "KVCache") -> int:
+    """Checks x as rows of heads; the distance between tokens in elements."""
+    if x.dtype is not torch.bfloat16 or x.get_device() != cache._dev:
         raise TypeError("%s must be a bfloat16 tensor on the cache's device" % name)
-    _need(x.dim() == 3 and x.shape[0] == tokens and x.shape[2] == cache.head_dim and
-          (heads is None or x.shape[1] == heads), "%s must be [tokens, heads, head_dim]" % name)
-    _need(x.stride(2) == 1 and x.stride(1) == cache.head_dim, "the heads of a token of %s must be contiguous" % name)
+    dim = cache.head_dim
+    if x.shape != (tokens, heads, dim):
+        raise ValueError("%s must be [tokens, heads, head_dim]" % name)
+    a, b, c = x.stride()
+    if (c != 1 or (b != dim and heads > 1)) and tokens:
+        raise ValueError("the heads of a token of %s must be contiguous" % name)
+    return a if tokens > 1 else heads * dim       # the distance of a single token is free
 
 
-def _ints(name: str, x: torch.Tensor, dtype, shape, cache: KVCache) -> None:
-    if x.dtype != dtype or x.device != cache.device:
+def _ints(name: str, x: torch.Tensor, dtype, shape, cache: "KVCache") -> int:
+    if x.dtype is not dtype or x.get_device() != cache._dev:
         raise TypeError("%s must be a %s tensor on the cache's device" % (name, str(dtype).replace("torch.", "")))
-    _need(tuple(x.shape) == shape and x.is_contiguous(), "%s must be contiguous %s" % (name, list(shape)))
+    if x.shape != shape or not x.is_contiguous():
+        raise ValueError("%s must be contiguous %s" % (name, list(shape)))
+    return x.data_ptr()
 
 
-def _status(status: Optional[torch.Tensor], cache: KVCache):
+def _status(status: Optional[torch.Tensor], cache: "KVCache"):
     if status is None:
         return None
-    if status.dtype != torch.int32 or status.device != cache.device:
+    if status.dtype is not torch.int32 or status.get_device() != cache._dev or status.numel() < 1:
         raise TypeError("status must be an int32 tensor on the cache's device")
     return status.data_ptr()
-
-
-def _ld(x: torch.Tensor) -> int:
-    # the distance of a single token is free
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -177,34 +181,36 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     rotated queries (q_out when given, which may be q), or None without q.
     fos_kv_append in include/fos.h has the rounding and the errors."""
     t = k.shape[0]
-    _rows("k", k, t, cache.heads, cache)
-    _rows("v", v, t, cache.heads, cache)
-    _ints("slots", slots, torch.int64, (t,), cache)
-    _need((cos_sin is None) == (positions is None), "positions and cos_sin belong together")
+    h = cache.heads
+    k_ld, v_ld = _rows("k", k, t, h, cache), _rows("v", v, t, h, cache)
+    at = _ints("slots", slots, torch.int64, (t,), cache)
     rot = None
+    q_ptr = out_ptr = None
+    q_ld = out_ld = hq = 0
     if cos_sin is not None:
-        _ints("positions", positions, torch.int32, (t,), cache)
+        _need(positions is not None, "cos_sin needs positions")
         _need(cos_sin.dim() == 2, "cos_sin must be [max_positions, dim]")
-        _ints("cos_sin", cos_sin, torch.float32, tuple(cos_sin.shape), cache)
-        rot = _RotaryC(cos_sin.data_ptr(), positions.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
-                       1 if interleaved else 0)
+        n, dim = cos_sin.shape
+        rot = ctypes.byref(_RotaryC(_ints("cos_sin", cos_sin, torch.float32, (n, dim), cache),
+                                    _ints("positions", positions, torch.int32, (t,), cache), n, dim,
+                                    1 if interleaved else 0))
+    else:
+        _need(positions is None, "positions need cos_sin")
     if q is not None:
         _need(rot is not None, "q is rotated: it needs positions and cos_sin")
-        _rows("q", q, t, None, cache)
+        _need(q.dim() == 3, "q must be [tokens, heads, head_dim]")
+        hq = q.shape[1]
+        q_ld = _rows("q", q, t, hq, cache)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            q_out, out_ld = q.new_empty((t, hq, cache.head_dim)), hq * cache.head_dim
         else:
-            _rows("q_out", q_out, t, q.shape[1], cache)
+            out_ld = _rows("q_out", q_out, t, hq, cache)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     else:
         _need(q_out is None, "q_out without q")
-    with _on(cache.device, stream) as s:
-        st = _lib().fos_kv_append(
-            cache._ref, fos.FMT[cache.fmt], k.data_ptr(), _ld(k), v.data_ptr(), _ld(v), t, slots.data_ptr(),
-            None if rot is None else ctypes.byref(rot), None if q is None else q.data_ptr(),
-            0 if q is None else _ld(q), None if q is None else q_out.data_ptr(), 0 if q is None else _ld(q_out),
-            0 if q is None else q.shape[1], _status(status, cache), s)
-    if st != 0:
-        raise fos.FosError(st, "fos_kv_append")
+    _call(cache, "fos_kv_append", _lib().fos_kv_append, stream,
+          (cache._ref, cache._fmt, k.data_ptr(), k_ld, v.data_ptr(), v_ld, t, at, rot, q_ptr, q_ld, out_ptr, out_ld,
+           hq, _status(status, cache)))
     return q_out
 
 
@@ -212,20 +218,19 @@ def kv_read(cache: KVCache, slots: torch.Tensor, out: Optional[Tuple[torch.Tenso
             status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The keys and values of slots (int64 [tokens]) as the cache holds them:
     two bf16 tensors [tokens, heads, head_dim], zeros for negative slots."""
-    t = slots.shape[0] if slots.dim() == 1 else -1
-    _ints("slots", slots, torch.int64, (max(t, 0),), cache)
+    _need(slots.dim() == 1, "slots must be [tokens]")
+    t = slots.shape[0]
+    at = _ints("slots", slots, torch.int64, (t,), cache)
     if out is None:
-        out = tuple(torch.empty(t, cache.heads, cache.head_dim, dtype=torch.bfloat16, device=cache.device)
-                    for _ in range(2))
-    for x in out:
-        _rows("out", x, t, cache.heads, cache)
-        _need(x.is_contiguous(), "out must be contiguous")
-    with _on(cache.device, stream) as s:
-        st = _lib().fos_kv_read(cache._ref, slots.data_ptr(), t, out[0].data_ptr(), out[1].data_ptr(),
-                                _status(status, cache), s)
-    if st != 0:
-        raise fos.FosError(st, "fos_kv_read")
-    return out[0], out[1]
+        out = slots.new_empty((2, t, cache.heads, cache.head_dim), dtype=torch.bfloat16).unbind(0)
+    else:
+        for x in out:
+            _rows("out", x, t, cache.heads, cache)
+            _need(x.is_contiguous(), "out must be contiguous")
+    k, v = out
+    _call(cache, "fos_kv_read", _lib().fos_kv_read, stream,
+          (cache._ref, at, t, k.data_ptr(), v.data_ptr(), _status(status, cache)))
+    return k, v
 
 
 def kv_attention_workspace_size(cache: KVCache, total_q: int, batch: int, q_heads: int, max_q: int,
@@ -250,39 +255,37 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, pages: tor
     return_lse (lse float32 [total_q, q_heads]).  Queries that see no key get
     zeros and -inf; rows of out and lse that belong to no sequence are left
     as they were.  fos_kv_attention in include/fos.h has the details."""
-    _rows("q", q, q.shape[0], None, cache)
+    _need(q.dim() == 3, "q must be [total_q, q_heads, head_dim]")
     t, hq = q.shape[0], q.shape[1]
+    q_ld = _rows("q", q, t, hq, cache)
     _need(hq > 0 and hq % cache.heads == 0, "q_heads must be a multiple of the cache's heads")
     _need(cu_q.dim() == 1 and cu_q.shape[0] >= 1, "cu_q must be [batch + 1]")
-    b = cu_q.shape[0] - 1
-    _ints("cu_q", cu_q, torch.int32, (b + 1,), cache)
     _need(pages.dim() == 2, "pages must be [batch, max_pages]")
-    _ints("pages", pages, torch.int32, (b, pages.shape[1]), cache)
-    _ints("kv_len", kv_len, torch.int32, (b,), cache)
     _need(window >= 0 and (causal or window == 0), "window needs causal")
+    b, most = cu_q.shape[0] - 1, pages.shape[1]
+    cu, table = _ints("cu_q", cu_q, torch.int32, (b + 1,), cache), _ints("pages", pages, torch.int32, (b, most), cache)
+    lens = _ints("kv_len", kv_len, torch.int32, (b,), cache)
     if out is None:
-        out = torch.empty(t, hq, cache.head_dim, dtype=torch.bfloat16, device=q.device)
+        out, out_ld = q.new_empty((t, hq, cache.head_dim)), hq * cache.head_dim
     else:
-        _rows("out", out, t, hq, cache)
+        out_ld = _rows("out", out, t, hq, cache)
+    lse_ptr = None
     if lse is not None:
-        _ints("lse", lse, torch.float32, (t, hq), cache)
+        lse_ptr = _ints("lse", lse, torch.float32, (t, hq), cache)
     elif return_lse:
-        lse = torch.empty(t, hq, dtype=torch.float32, device=q.device)
-    with _on(cache.device, stream) as s:
-        L = _lib()
-        need = L.fos_kv_attention_workspace_size(cache._ref, t, b, hq, max_q, pages.shape[1])
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                workspace.record_stream(stream)
-        elif workspace is not None:
-            _need(workspace.device == cache.device, "workspace must be on the cache's device")
-        st = L.fos_kv_attention(
-            cache._ref, q.data_ptr(), _ld(q), t, hq, cu_q.data_ptr(), b, pages.data_ptr(), pages.shape[1],
-            kv_len.data_ptr(), max_q, 1.0 / math.sqrt(cache.head_dim) if scale is None else scale,
-            1 if causal else 0, window, out.data_ptr(), _ld(out), None if lse is None else lse.data_ptr(),
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _status(status, cache), s)
-    if st != 0:
-        raise fos.FosError(st, "fos_kv_attention")
+        lse = q.new_empty((t, hq), dtype=torch.float32)
+        lse_ptr = lse.data_ptr()
+    L = _lib()
+    need = L.fos_kv_attention_workspace_size(cache._ref, t, b, hq, max_q, most)
+    if workspace is None and need:
+        workspace = q.new_empty((need,), dtype=torch.uint8)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif workspace is not None:
+        _need(workspace.get_device() == cache._dev, "workspace must be on the cache's device")
+        need = workspace.numel() * workspace.element_size()
+    _call(cache, "fos_kv_attention", L.fos_kv_attention, stream,
+          (cache._ref, q.data_ptr(), q_ld, t, hq, cu, b, table, most, lens, max_q,
+           cache._scale if scale is None else scale, 1 if causal else 0, window, out.data_ptr(), out_ld, lse_ptr,
+           None if workspace is None else workspace.data_ptr(), need, _status(status, cache)))
     return (out, lse) if return_lse else out
