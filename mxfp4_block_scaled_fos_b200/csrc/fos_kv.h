@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "fos.h"
 
 namespace fos {
@@ -56,6 +58,26 @@ struct KvAttnArgs {
   long long window;                       // 0: none
   float scale_log2;                       // scale * log2(e)
   uint32_t* status;
+};
+
+// What a launch asks of the current device, asked once for each: the SMs, and
+// a kernel's shared memory above the default.
+struct KvDevices {
+  std::atomic<int> sms[64] = {};
+  cudaError_t get(const void* kernel, int smem, int* out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int n = dev < 64 ? sms[dev].load(std::memory_order_acquire) : 0;
+    if (n == 0) {
+      if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+          (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+        return e;
+      if (dev < 64) sms[dev].store(n, std::memory_order_release);
+    }
+    *out = n;
+    return cudaSuccess;
+  }
 };
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, int fmt, bool interleaved, cudaStream_t st);

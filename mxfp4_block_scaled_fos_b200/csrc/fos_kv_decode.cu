@@ -787,55 +787,81 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   }
 }
 
-// Joins an item that several shares hold: the CTA of the share in which the
-// item ends adds the partial results in the order of the tokens.
+// Joins an item that several shares hold: the CTAs of those shares (but one
+// that the item only ends) take its rows in turn.  The warps of a CTA take a
+// row each, or several share a row's partial results; every sum is in the
+// order of the tokens within a warp and over the warps in theirs.
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttnArgs a, const float* part) {
   using C = Cfg<D, NT>;
   constexpr int R = C::kRows;
   __shared__ Plan plan;
   __shared__ long long sums[kWarps];
+  __shared__ float4 s_o[kWarps][D / 4];
+  __shared__ float2 s_ml[kWarps];
   make_plan<R>(a, blockIdx.x, gridDim.x, &plan, sums, false);
   const Split split(plan.total, gridDim.x);
   const long long first = plan.first, last = split.first(blockIdx.x + 1);
   Item it;
-  const bool mine = first < last && find_item<R>(a, first, plan.b, plan.at, it) && first > it.start &&
-                    it.start + it.s.tiles <= last;
+  bool mine = first < last && find_item<R>(a, first, plan.b, plan.at, it);
+  int c0 = 0, c1 = 0, lead = 0;
+  if (mine) {
+    c0 = split.of(it.start);
+    c1 = split.of(it.start + it.s.tiles - 1);
+    lead = split.first(c0) < it.start ? c0 + 1 : c0;   // the first share that begins with this item or inside it
+    mine = c1 > c0;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!mine) return;
-  // the item is the first segment of every share but the one that it begins inside
-  const int c0 = split.of(it.start), n = blockIdx.x - c0 + 1;
-  const float* p0 = part + (long long)(2 * c0 + (split.first(c0) < it.start ? 1 : 0)) * C::kPart;
-  const float* p1 = part + (long long)(2 * c0) * C::kPart;
-  for (int x = threadIdx.x; x < R * (D / 4); x += kThreads) {
-    const int r = x / (D / 4), d = (x - r * (D / 4)) * 4;
-    if (it.rt * R + r >= it.n * a.group) continue;
+  const int ctas = c1 - lead + 1, n = c1 - c0 + 1;     // CTAs on the item, its partial results
+  const int rows = (R + ctas - 1) / ctas;              // of this CTA: r = blockIdx.x - lead + ctas * k
+  const int wide = rows >= 8 ? 8 : rows > 2 ? 4 : rows;   // rows at a time
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int teams = kWarps / wide, team = warp / wide;
+  const float* p0 = part + (long long)(2 * c0 + (lead > c0 ? 1 : 0)) * C::kPart;
+  for (int k0 = 0; k0 < rows; k0 += wide) {
+    const int r = blockIdx.x - lead + ctas * (k0 + warp % wide);
+    const bool live = r < R && it.rt * R + r < it.n * a.group;
     float M = -CUDART_INF_F, L = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (live && lane < D / 4) {
 #pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float* p = s ? p1 + (long long)(2 * s) * C::kPart : p0;
-      const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
-      const float pm = p[R * D + r], pl = p[R * D + R + r], top = fmaxf(M, pm);
-      const float f = M == top ? 1.0f : ex2(M - top), k = pm == top ? 1.0f : ex2(pm - top);
-      L = L * f + pl * k;
-      o.x = o.x * f + v.x * k; o.y = o.y * f + v.y * k; o.z = o.z * f + v.z * k; o.w = o.w * f + v.w * k;
-      M = top;
+      for (int s = team; s < n; s += teams) {
+        const float* p = s ? part + (long long)(2 * (c0 + s)) * C::kPart : p0;
+        const float4 v = *reinterpret_cast<const float4*>(p + r * D + 4 * lane);
+        const float pm = p[R * D + r], pl = p[R * D + R + r], top = fmaxf(M, pm);
+        const float f = M == top ? 1.0f : ex2(M - top), k = pm == top ? 1.0f : ex2(pm - top);
+        L = L * f + pl * k;
+        o.x = o.x * f + v.x * k; o.y = o.y * f + v.y * k; o.z = o.z * f + v.z * k; o.w = o.w * f + v.w * k;
+        M = top;
+      }
+      s_o[warp][lane] = o;
+      if (lane == 0) s_ml[warp] = make_float2(M, L);
     }
-    write_row(a, it, it.rt * R + r, d, D, o, M, L);
+    __syncthreads();
+    if (live && team == 0 && lane < D / 4) {
+      for (int t = 1; t < teams && t < n; ++t) {
+        const float2 ml = s_ml[warp + t * wide];
+        const float4 v = s_o[warp + t * wide][lane];
+        const float top = fmaxf(M, ml.x);
+        const float f = M == top ? 1.0f : ex2(M - top), k = ml.x == top ? 1.0f : ex2(ml.x - top);
+        L = L * f + ml.y * k;
+        o.x = o.x * f + v.x * k; o.y = o.y * f + v.y * k; o.z = o.z * f + v.z * k; o.w = o.w * f + v.w * k;
+        M = top;
+      }
+      write_row(a, it, it.rt * R + r, 4 * lane, D, o, M, L);
+    }
+    __syncthreads();
   }
 }
 
 template <int D, int NT>
 cudaError_t launch(const KvAttnArgs& a, float* part, cudaStream_t st) {
   using C = Cfg<D, NT>;
-  int dev = 0, sms = 0;
-  cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
-      (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(k_kv_decode<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) !=
-          cudaSuccess)
-    return e;
+  static KvDevices devices;
+  int sms = 0;
+  cudaError_t e = devices.get((const void*)k_kv_decode<D, NT>, C::kSmem, &sms);
+  if (e != cudaSuccess) return e;
   const int ctas = C::kCtas * sms < kMaxCtas ? C::kCtas * sms : kMaxCtas;
   k_kv_decode<D, NT><<<ctas, kThreads, C::kSmem, st>>>(a, part);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

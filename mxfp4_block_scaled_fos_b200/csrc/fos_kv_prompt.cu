@@ -609,7 +609,9 @@ long long item_bound(long long total_q, long long batch, long long group) {
 template <int D>
 cudaError_t launch(const KvAttnArgs& a, int splits, float* part, cudaStream_t st) {
   using C = Cfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(k_kv_prompt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static KvDevices devices;
+  int sms = 0;
+  cudaError_t e = devices.get((const void*)k_kv_prompt<D>, C::kSmem, &sms);
   if (e != cudaSuccess) return e;
   const long long grid = item_bound(a.total_q, a.batch, a.group) * a.p.heads;
   if (grid > 0x7fffffffll) return cudaErrorNotSupported;
