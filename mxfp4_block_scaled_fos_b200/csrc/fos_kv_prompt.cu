@@ -73,35 +73,43 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+// Operand descriptors, 128-byte swizzle, as two words.  Low: the address and,
+// for the MN-major values, the distance of its groups of 64 (unused, 1, for
+// K-major).  High: 1024 bytes between groups of 8 rows (K-major) or tokens.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return ((addr & 0x3FFFF) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr, uint32_t half) {
+  return ((addr & 0x3FFFF) >> 4) | ((half >> 4) << 16);
 }
 
-// K-major operand, 128-byte swizzle: 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-// MN-major operand, 128-byte swizzle: groups of 8 tokens 1024 bytes apart,
-// groups of 64 values `half` bytes apart.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t half) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(half >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The MMAs and commits run converged, predicated on one lane, so that their
+// operands stay in uniform registers: issued from a branch of one thread an
+// MMA took 75 cycles, more than the 64 that the tensor core needs for it.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(lead), "r"(kDescHi) : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 db, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(lead), "r"(kDescHi) : "memory");
+}
+
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      :: "r"(bar), "r"(lead) : "memory");
 }
 
 #define FOS_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
@@ -346,13 +354,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
           for (int k = 0; k < 128; ++k)
             if (!((v[k >> 5] >> (k & 31)) & 1u) || tok0 + k >= hi || tok0 + k < lo) s[k] = 0xff800000u;
         }
-        float x0 = __uint_as_float(s[0]), x1 = __uint_as_float(s[1]);
+        float xm[4];
 #pragma unroll
-        for (int k = 2; k < 128; k += 2) {
-          x0 = fmaxf(x0, __uint_as_float(s[k]));
-          x1 = fmaxf(x1, __uint_as_float(s[k + 1]));
+        for (int c = 0; c < 4; ++c) {
+          xm[c] = fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 4]));
+#pragma unroll
+          for (int k = 8 + c; k < 128; k += 8)
+            xm[c] = fmaxf(fmaxf(xm[c], __uint_as_float(s[k])), __uint_as_float(s[k + 4]));
         }
-        x0 = fmaxf(x0, x1);
+        const float x0 = fmaxf(fmaxf(xm[0], xm[1]), fmaxf(xm[2], xm[3]));
         const bool raise = x0 > m && (m == -CUDART_INF_F || (x0 - m) * rs > kSlack);
         if (__any_sync(~0u, raise)) {
           const float keep = !raise ? 1.0f : m == -CUDART_INF_F ? 0.0f : ex2((m - x0) * rs);
@@ -445,98 +455,107 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     const int row = tid - 256;
     const int32_t* pages = a.pages + (long long)it.b * a.max_pages;
-    long long co = 0, so = 0;      // this thread's token of a tile in the pools
-    bool seen = false;
-    auto locate = [&](int j) {
+    // this thread's token of a tile, two tiles ahead of the conversion: its
+    // page's id; one ahead: where it is in the pools, and its codes and scales
+    auto page_of = [&](int j) {
       const int tok = tok_base + j * kTileTok + row;
-      seen = tok >= it.lo && tok < it.hi;
-      if (seen) {
-        const int page = __ldg(pages + (tok >> a.p.page_shift));
-        if (page < 0 || page >= a.p.num_pages) {
-          seen = false;
+      int page = -1;
+      if (j < J && tok >= it.lo && tok < it.hi) {
+        page = __ldg(pages + (tok >> a.p.page_shift));
+        if ((uint32_t)page >= (uint32_t)a.p.num_pages) {
+          page = -1;
           if (a.status) atomicOr(a.status, FOS_STATUS_INDEX);
-        } else {
-          const long long pr = ((long long)h << a.p.page_shift) + (tok & ((1 << a.p.page_shift) - 1));
-          co = page * a.p.codes_stride + pr * (D / 2);
-          so = page * a.p.scales_stride + pr * (D / 16);
         }
       }
+      return page;
+    };
+    unsigned long long co = 0, so = 0;
+    bool seen = false;
+    auto locate = [&](int j, int page) {
+      const uint32_t r = ((uint32_t)h << a.p.page_shift) +
+                         ((uint32_t)(tok_base + j * kTileTok + row) & ((1u << a.p.page_shift) - 1));
+      seen = page >= 0;
+      co = (unsigned long long)(uint32_t)page * a.p.codes_stride32 + r * (D / 2);
+      so = (unsigned long long)(uint32_t)page * a.p.scales_stride32 + r * (D / 16);
     };
     Raw<D> k, v;
+    bool seen_k = false;           // of the keys in k
+    int page = -1;
     if (J > 0) {
-      locate(0);
+      locate(0, page_of(0));
+      seen_k = seen;
       load_raw<D>(k, a.p.kc + co, a.p.ks + so, seen);
       load_raw<D>(v, a.p.vc + co, a.p.vs + so, seen);
+      page = page_of(1);
     }
 #pragma unroll 1
     for (int j = 0; j < J; ++j) {
       const int s = j & 1;
       const uint32_t parity = ((j >> 1) & 1) ^ 1;
+      locate(j + 1, page);
+      page = page_of(j + 2);
       if (j >= 2 && !__all_sync(~0u, mbar_wait(bar + 8 * (B_KEMPTY + s), parity, fail))) break;
-      const uint32_t mask = __ballot_sync(~0u, seen);
+      const uint32_t mask = __ballot_sync(~0u, seen_k);
       if (lane == 0) reinterpret_cast<uint32_t*>(smem + C::kOffValid)[(j & 3) * 4 + (warp & 3)] = mask;
       store_raw<D>(k, smem + C::kOffK + s * C::kOperand, row);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + 8 * (B_KFULL + s));
-      if (j + 1 < J) {
-        locate(j + 1);
-        load_raw<D>(k, a.p.kc + co, a.p.ks + so, seen);
-      }
+      load_raw<D>(k, a.p.kc + co, a.p.ks + so, seen);
+      seen_k = seen;
       if (j >= 2 && !__all_sync(~0u, mbar_wait(bar + 8 * (B_VEMPTY + s), parity, fail))) break;
       store_raw<D>(v, smem + C::kOffV + s * C::kOperand, row);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + 8 * (B_VFULL + s));
-      if (j + 1 < J) load_raw<D>(v, a.p.vc + co, a.p.vs + so, seen);
+      load_raw<D>(v, a.p.vc + co, a.p.vs + so, seen);
     }
   } else {
     // ---------------------------------------------------------------- MMAs
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 12 && lane == 0 && J > 0) {
-      auto scores = [&](int t, int j) {
-        const uint32_t q = sbase + C::kOffQ + t * C::kOperand, k = sbase + C::kOffK + (j & 1) * C::kOperand;
+    if (warp == 12 && J > 0) {
+      const uint32_t lead = lane == 0;
+      const uint32_t dq = desc_k(sbase + C::kOffQ), dk = desc_k(sbase + C::kOffK);
+      const uint32_t dv = desc_mn(sbase + C::kOffV, C::kHalf);
+      constexpr uint32_t kStep = C::kOperand >> 4;    // from one tile or stage to the next
+      auto scores = [&](uint32_t t, uint32_t stage) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t at = (i >> 2) * C::kHalf + (i & 3) * 32;
-          mma_ss(tmem + C::kColS + 128 * t, desc_k(q + at), desc_k(k + at), C::kIdescS, i > 0);
+          const uint32_t at = ((i >> 2) * C::kHalf + (i & 3) * 32) >> 4;
+          mma_ss(tmem + C::kColS + 128 * t, dq + t * kStep + at, dk + stage * kStep + at, C::kIdescS, i > 0, lead);
         }
-        commit(bar + 8 * (B_S + t));
+        commit(bar + 8 * (B_S + t), lead);
       };
       bool ok = mbar_wait(bar + 8 * B_Q, 0, fail) && mbar_wait(bar + 8 * B_KFULL, 0, fail);
       if (ok) {
         fence_after();
         for (int t = 0; t < nt; ++t) scores(t, 0);
-        commit(bar + 8 * B_KEMPTY);
+        commit(bar + 8 * B_KEMPTY, lead);
       }
+#pragma unroll 1
       for (int j = 0; ok && j < J; ++j) {
-        const int s = j & 1, s1 = s ^ 1;
+        const uint32_t s = j & 1, s1 = s ^ 1;
+        // keys and values are there long before the weights as a rule
+        ok = mbar_wait(bar + 8 * (B_VFULL + s), (j >> 1) & 1, fail) &&
+             (j + 1 >= J || mbar_wait(bar + 8 * (B_KFULL + s1), ((j + 1) >> 1) & 1, fail));
+#pragma unroll 1
         for (int t = 0; ok && t < nt; ++t) {
-          if (t == 0) ok = mbar_wait(bar + 8 * (B_VFULL + s), (j >> 1) & 1, fail);
-          ok = ok && mbar_wait(bar + 8 * (B_P + t), j & 1, fail);
+          ok = mbar_wait(bar + 8 * (B_P + t), j & 1, fail);
           if (!ok) break;
           fence_after();
-          const uint32_t v = sbase + C::kOffV + s * C::kOperand;
 #pragma unroll
           for (int i = 0; i < kTileTok / 16; ++i)
-            mma_ts(tmem + C::kColO + 128 * t, tmem + C::kColS + 128 * t + 8 * i, desc_mn(v + i * 2048, C::kHalf),
-                   C::kIdescO, j > 0 || i > 0);
-          if (t == nt - 1) commit(bar + 8 * (B_VEMPTY + s));
-          if (j + 1 < J) {
-            if (t == 0) {
-              ok = mbar_wait(bar + 8 * (B_KFULL + s1), ((j + 1) >> 1) & 1, fail);
-              if (!ok) break;
-              fence_after();
-            }
-            scores(t, j + 1);
-            if (t == nt - 1) commit(bar + 8 * (B_KEMPTY + s1));
-          } else {
-            commit(bar + 8 * (B_O + t));
-          }
+            mma_ts(tmem + C::kColO + 128 * t, tmem + C::kColS + 128 * t + 8 * i, dv + s * kStep + (i * 2048 >> 4),
+                   C::kIdescO, j > 0 || i > 0, lead);
+          if (j + 1 < J) scores(t, s1);
+          else           commit(bar + 8 * (B_O + t), lead);
         }
+        // of tile j, all products; of tile j + 1, the scores
+        commit(bar + 8 * (B_VEMPTY + s), lead);
+        if (j + 1 < J) commit(bar + 8 * (B_KEMPTY + s1), lead);
       }
       if (!ok) {   // let what was issued finish before the tensor memory is freed
-        commit(bar + 8 * B_DRAIN);
+        commit(bar + 8 * B_DRAIN, lead);
         for (uint32_t i = 0; i < kWaitLimit; ++i) {
           uint32_t done;
           asm volatile(
