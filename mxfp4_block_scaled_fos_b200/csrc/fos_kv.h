@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "fos.h"
+#include "fos_internal.h"
 
 namespace fos {
 
@@ -41,6 +42,7 @@ struct KvReadArgs {
   KvPool p;
   const int64_t* slots;
   int tokens;
+  int token0;                             // of this launch
   uint16_t *k, *v;
   uint32_t* status;
 };

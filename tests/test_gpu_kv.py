@@ -69,7 +69,10 @@ def test_append_and_read_match_the_oracle(dim, page, rot, inter, fmt, tokens, he
     x = (torch.randn(tokens, q_heads + 2 * heads + 1, dim, generator=g)).to(torch.bfloat16)
     x[0, -2:, :16] = 0
     q, k, v = x[:, :q_heads], x[:, q_heads:q_heads + heads], x[:, q_heads + heads:q_heads + 2 * heads]
-    xd = x.to(dev)
+    # 32-byte aligned rows, or (odd numbers of tokens) rows that are only 16-byte aligned
+    pad = 8 * (tokens % 2)
+    xd = torch.zeros(tokens, x.shape[1] * dim + pad, dtype=torch.bfloat16, device=dev)[:, pad:].unflatten(1, x.shape[1:])
+    xd.copy_(x)
     qd, kd, vd = (xd[:, a:b] for a, b in ((0, q_heads), (q_heads, q_heads + heads),
                                           (q_heads + heads, q_heads + 2 * heads)))
     slots = torch.randperm(n * page, generator=g)[:tokens].to(torch.int64)
