@@ -79,16 +79,103 @@ __device__ __forceinline__ void load32(const uint16_t* p, uint4 (&w)[2]) {
 }
 
 // Append.  A token's rows are its query heads, key heads and value heads; a
-// thread takes a 16-value block of one row, dim/16 neighbouring lanes a row.
-// With halves as pairs the other value of each pair is rot/2 further on, in a
-// block that another lane of the row holds too: it is loaded again, from L1,
-// and so are the angles, which the rows of a token share.  (Keeping the
-// angles in registers through several rows of a token cost more in occupancy
-// than it saved in loads.)  Memory-bound for long prompts, where the queries
-// are most of the bytes; launch and latency for a decoding step.
+// thread takes two 16-value blocks of one row, with dim/32 neighbouring lanes
+// a row.  With halves as pairs (rot a multiple of 32) they are a block of
+// first values and the block of their partners rot/2 further on, so that
+// every value is loaded and widened once and an angle serves two of them;
+// otherwise they are neighbours.  Products are fma(x, c, -0) in pairs: rounded
+// by themselves (see the f32x2 helpers), two to an instruction.
+// Memory-bound for long prompts, where the queries are most of the bytes;
+// launch and latency for a decoding step.
 // WIDE: all rows 32-byte aligned, one load and one store a block.
 template <bool F46, bool INTER, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 6) k_kv_append(const KvAppendArgs a) {
+__global__ void __launch_bounds__(256, 4) k_kv_append(const KvAppendArgs a) {
+  const int lanes = a.p.dim >> 5;
+  const int x = blockIdx.y * blockDim.x + threadIdx.x;
+  const int r = x / lanes, p = x & (lanes - 1);
+  const int t = blockIdx.x;
+  const int kind = r < a.q_heads ? 0 : r < a.q_heads + a.p.heads ? 1 : r < a.q_heads + 2 * a.p.heads ? 2 : 3;
+  const int h = kind == 0 ? r : kind == 1 ? r - a.q_heads : r - a.q_heads - a.p.heads;
+  const int half = a.rot >> 1;
+  const bool turned = a.table && kind < 2 && 32 * p < a.rot;
+  const int d0 = !INTER && 32 * p < a.rot ? 16 * p : 32 * p;             // the blocks' first values
+  const int d1 = !INTER && 32 * p < a.rot ? d0 + half : d0 + 16;
+  uint4 w[2][2];
+  const uint16_t* src = nullptr;
+  if (kind < 3) {
+    src = kind == 0 ? a.q + (long long)t * a.q_ld
+                    : kind == 1 ? a.k + (long long)t * a.k_ld : a.v + (long long)t * a.v_ld;
+    src += h * a.p.dim;
+    load32<WIDE>(src + d0, w[0]);
+    load32<WIDE>(src + d1, w[1]);
+  }
+  const long long slot = a.slots[t];
+  const long long page = slot >> a.p.page_shift;
+  bool write = slot >= 0, turn_ok = true;
+  if (write && page >= a.p.num_pages) {
+    write = false;
+    if (x == 0 && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
+  }
+  if (a.table) {
+    const int pos = a.positions[t];
+    if (pos < 0 || pos >= a.max_positions) {
+      if (x == 0 && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
+      write = turn_ok = false;
+    } else if (turned) {
+      const float* row = a.table + (long long)pos * a.rot;
+      const float2 nz = make_float2(a.neg_zero, a.neg_zero);
+      uint32_t(&W)[2][8] = reinterpret_cast<uint32_t(&)[2][8]>(w);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {       // four pairs of each of two words of either block (INTER: of one word)
+        const int i = INTER ? (d0 >> 1) + 4 * q : d0 + 4 * q;
+        if (INTER && 2 * i >= a.rot) continue;
+        const float4 c = __ldg(reinterpret_cast<const float4*>(row + i));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + i));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {     // the angles of pairs i + 2 e, i + 2 e + 1
+          const float2 c2 = e ? make_float2(c.z, c.w) : make_float2(c.x, c.y);
+          const float2 s2 = e ? make_float2(s.z, s.w) : make_float2(s.x, s.y);
+          // INTER: pair i is word i of the thread's 16
+          uint32_t& wa = INTER ? W[q >> 1][4 * (q & 1) + 2 * e] : W[0][2 * q + e];
+          uint32_t& wb = INTER ? W[q >> 1][4 * (q & 1) + 2 * e + 1] : W[1][2 * q + e];
+          const float2 u = INTER ? make_float2(bf_lo(wa), bf_lo(wb)) : make_float2(bf_lo(wa), bf_hi(wa));
+          const float2 v = INTER ? make_float2(bf_hi(wa), bf_hi(wb)) : make_float2(bf_lo(wb), bf_hi(wb));
+          const float2 a2 = sub2(fma2(u, c2, nz), fma2(v, s2, nz));
+          const float2 b2 = add2(fma2(v, c2, nz), fma2(u, s2, nz));
+          wa = INTER ? pack_bf16(a2.x, b2.x) : pack_bf16(a2.x, a2.y);
+          wb = INTER ? pack_bf16(a2.y, b2.y) : pack_bf16(b2.x, b2.y);
+        }
+      }
+    }
+  }
+  if (kind == 0 && turn_ok) {
+    uint16_t* dst = a.q_out + (long long)t * a.q_out_ld + h * a.p.dim;
+    store32<WIDE>(dst + d0, w[0]);
+    store32<WIDE>(dst + d1, w[1]);
+  } else if ((kind == 1 || kind == 2) && write) {
+    const TScale ts = make_tscale(__ldg((kind == 1 ? a.p.kst : a.p.vst) + h));
+    const long long row = ((long long)h << a.p.page_shift) + (slot & ((1 << a.p.page_shift) - 1));
+    uint8_t* codes = (kind == 1 ? a.p.kc : a.p.vc) + page * a.p.codes_stride + row * (a.p.dim >> 1);
+    uint8_t* scales = (kind == 1 ? a.p.ks : a.p.vs) + page * a.p.scales_stride + row * (a.p.dim >> 4);
+    bool good = true;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int d = b ? d1 : d0;
+      uint32_t cw[2], sc;
+      good &= quantize_block<F46>(w[b], ts, a.neg_zero, cw, sc);
+      *reinterpret_cast<uint2*>(codes + (d >> 1)) = make_uint2(cw[0], cw[1]);
+      scales[d >> 4] = (uint8_t)sc;
+    }
+    if (!good && a.status) atomicOr(a.status, FOS_STATUS_NONFINITE);
+  }
+}
+
+// The same for halves as pairs whose partners are not whole blocks apart (rot
+// not a multiple of 32): a thread has one block, and the other value of each
+// pair, rot/2 further on or back, is loaded again from a row that it shares
+// with its lanes of the warp; 8 values at a time (rot/2 is a multiple of 8).
+template <bool F46, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 6) k_kv_append_odd(const KvAppendArgs a) {
   const int nb = a.p.dim >> 4;
   const int bi = threadIdx.x & (nb - 1);
   const int r = blockIdx.y * (kThreads / nb) + threadIdx.x / nb;
@@ -103,15 +190,13 @@ __global__ void __launch_bounds__(kThreads, 6) k_kv_append(const KvAppendArgs a)
                                     : kind == 1 ? a.k + (long long)t * a.k_ld : a.v + (long long)t * a.v_ld;
     src += (long long)h * a.p.dim + d0;
     load32<WIDE>(src, w);
-    // value d is turned with d + rot/2 or d - rot/2, the same way for 8 values
-    // at a time (rot/2 is a multiple of 8); INTER: with its neighbour
     if (a.table && kind < 2) {
 #pragma unroll
       for (int hb = 0; hb < 2; ++hb) {
         const int d = d0 + 8 * hb;
         if (d >= a.rot) continue;
         part[hb] = d < half ? half : -half;
-        if (!INTER) y[hb] = *reinterpret_cast<const uint4*>(src + 8 * hb + part[hb]);
+        y[hb] = *reinterpret_cast<const uint4*>(src + 8 * hb + part[hb]);
       }
     }
   }
@@ -134,27 +219,16 @@ __global__ void __launch_bounds__(kThreads, 6) k_kv_append(const KvAppendArgs a)
         if (!part[hb]) continue;
         uint32_t x[4] = {w[hb].x, w[hb].y, w[hb].z, w[hb].w};
         const int d = d0 + 8 * hb;
-        if (INTER) {
-          const float4 c = __ldg(reinterpret_cast<const float4*>(row + (d >> 1)));
-          const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + (d >> 1)));
-          const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+        const bool first = part[hb] > 0;
+        float c[8], s[8];
+        load8(row + (first ? d : d - half), c);
+        load8(row + half + (first ? d : d - half), s);
+        const uint32_t z[4] = {y[hb].x, y[hb].y, y[hb].z, y[hb].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float u = bf_lo(x[k]), v = bf_hi(x[k]);
-            x[k] = pack_bf16(turn(u, cc[k], v, -ss[k]), turn(v, cc[k], u, ss[k]));
-          }
-        } else {
-          const bool first = part[hb] > 0;
-          float c[8], s[8];
-          load8(row + (first ? d : d - half), c);
-          load8(row + half + (first ? d : d - half), s);
-          const uint32_t z[4] = {y[hb].x, y[hb].y, y[hb].z, y[hb].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float s0 = first ? -s[2 * k] : s[2 * k], s1 = first ? -s[2 * k + 1] : s[2 * k + 1];
-            x[k] = pack_bf16(turn(bf_lo(x[k]), c[2 * k], bf_lo(z[k]), s0),
-                             turn(bf_hi(x[k]), c[2 * k + 1], bf_hi(z[k]), s1));
-          }
+        for (int k = 0; k < 4; ++k) {
+          const float s0 = first ? -s[2 * k] : s[2 * k], s1 = first ? -s[2 * k + 1] : s[2 * k + 1];
+          x[k] = pack_bf16(turn(bf_lo(x[k]), c[2 * k], bf_lo(z[k]), s0),
+                           turn(bf_hi(x[k]), c[2 * k + 1], bf_hi(z[k]), s1));
         }
         w[hb] = make_uint4(x[0], x[1], x[2], x[3]);
       }
@@ -229,12 +303,22 @@ inline bool aligned32(const void* p, long long ld) { return (uintptr_t)p % 32 ==
 
 template <bool F46, bool INTER>
 cudaError_t append(const KvAppendArgs& a, cudaStream_t st) {
-  const int lanes = kThreads / (a.p.dim / 16), rows = a.q_heads + 2 * a.p.heads;
-  const dim3 grid(a.tokens, (rows + lanes - 1) / lanes);
+  const int rows = a.q_heads + 2 * a.p.heads;
   const bool wide = aligned32(a.k, a.k_ld) && aligned32(a.v, a.v_ld) &&
                     (!a.q || (aligned32(a.q, a.q_ld) && aligned32(a.q_out, a.q_out_ld)));
-  if (wide) k_kv_append<F46, INTER, true><<<grid, kThreads, 0, st>>>(a);
-  else      k_kv_append<F46, INTER, false><<<grid, kThreads, 0, st>>>(a);
+  if (!INTER && a.rot % 32) {
+    const int lanes = kThreads / (a.p.dim / 16);
+    const dim3 grid(a.tokens, (rows + lanes - 1) / lanes);
+    if (wide) k_kv_append_odd<F46, true><<<grid, kThreads, 0, st>>>(a);
+    else      k_kv_append_odd<F46, false><<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  // a token's rows in CTAs of equal size, up to 256 threads
+  const int all = rows * (a.p.dim / 32), ctas = (all + 255) / 256;
+  const int threads = ((all + ctas - 1) / ctas + 31) / 32 * 32;
+  const dim3 grid(a.tokens, ctas);
+  if (wide) k_kv_append<F46, INTER, true><<<grid, threads, 0, st>>>(a);
+  else      k_kv_append<F46, INTER, false><<<grid, threads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
