@@ -44,6 +44,11 @@ namespace {
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kSlice = 16, kTile = 128;               // tokens of one copy, of a tile
 constexpr int kStagesK = 2, kStagesV = 3;             // tiles of a group in shared memory
+// What beginning an item costs, in tiles.  Without it a share of many short
+// items takes far longer than its tiles say: 64 ragged contexts of up to
+// 16384 tokens 209 us with 0, 155 with 3, 151 with 8, 152 with 12; 48 windows
+// of 1000 tokens 47, 35, 31, 31 us.
+constexpr int kOver = 8;
 constexpr int kMaxCtas = 320;                         // shares: two CTAs on each of up to 160 SMs
 constexpr float kNone = -1e30f;                       // the maximum of a row that has seen nothing
 constexpr uint32_t kWaitLimit = 1u << 20;
@@ -62,10 +67,10 @@ struct Cfg {
   static constexpr int kQ = kCols * D / 2;                               // one set of digits
   static constexpr int kOffP = kOffQ + 2 * kQ;                           // weights, [warp][32 tokens][rows] f16
   static constexpr int kOffStat = kOffP + kWarps * 32 * kRows * 2;       // m, l [warps][rows]
-  static constexpr int kOffRow = kOffStat + 2 * kWarps * kRows * 4;      // rs, hi, lo [rows]
-  static constexpr int kOffBar = kOffRow + 3 * kRows * 4;                // of a group: scores done, keys ready
+  static constexpr int kOffRow = kOffStat + 2 * kWarps * kRows * 4;      // rs, hi, lo, query, head [rows]
+  static constexpr int kOffBar = kOffRow + 5 * kRows * 4;                // of a group: scores done, keys ready
   static constexpr int kOffPlan = kOffBar + 2 * 16 + 16;
-  static constexpr int kSmem = kOffPlan + 64 + kWarps * 8 + 1024;        // + alignment slack
+  static constexpr int kSmem = kOffPlan + 128 + kWarps * 8 + 1024;        // + alignment slack
   static constexpr int kPart = kRows * (D + 2);                          // floats of one partial result
   static constexpr uint32_t kTmemCols = NT == 1 ? 128 : 256;
   static constexpr uint32_t kColSFA = 2 * kCols, kColSFB = kColSFA + 16; // + 8 * group; 4 each for both digit sets
@@ -193,7 +198,11 @@ struct Span {
 template <int ROWS>
 __device__ __forceinline__ Span span_of(const KvAttnArgs& a, int n, int len, int rt) {
   Span s;
-  const int first = rt * ROWS / a.group, last = min(n * a.group - 1, rt * ROWS + ROWS - 1) / a.group;
+  int first = 0, last = n - 1;
+  if (n * a.group > ROWS) {
+    first = rt * ROWS / a.group;
+    last = min(n * a.group - 1, rt * ROWS + ROWS - 1) / a.group;
+  }
   s.hi = query_hi(a, n, len, last);
   s.lo = query_lo(a, query_hi(a, n, len, first));
   s.base = s.lo & ~(kSlice - 1);
@@ -201,50 +210,84 @@ __device__ __forceinline__ Span span_of(const KvAttnArgs& a, int n, int len, int
   return s;
 }
 
-template <int ROWS>
-__device__ __forceinline__ long long tiles_of(const KvAttnArgs& a, int n, int len) {
-  const int nrt = (n * a.group + ROWS - 1) / ROWS;
-  long long t = 0;
-  for (int rt = 0; rt < nrt; ++rt) t += span_of<ROWS>(a, n, len, rt).tiles;
-  return t * a.p.heads;
+// a / b for a >= 0, b > 0, short where both fit 32 bits
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
+  return a / b;
 }
 
-// Where a share of the tiles begins.
-struct Plan {
-  long long total, first, at;   // all tiles, this share's first, the first of sequence b
-  int b;
-};
-
-// Share s of `shares` begins at tile s * base + min(s, rest).
+// Work is counted in tiles, with kOver of them before each item's first for
+// what it costs to begin one.  Share s of `shares` begins at s * base +
+// min(s, rest); a share that begins in an item's kOver begins with its tile 0.
 struct Split {
   long long base;
   int rest;
   __device__ __forceinline__ Split(long long total, int shares) {
-    base = total / shares;
+    base = quotient(total, shares);
     rest = (int)(total - base * shares);
   }
   __device__ __forceinline__ long long first(int s) const { return base * s + min(s, rest); }
-  // the share that holds tile x
+  // the share that holds x
   __device__ __forceinline__ int of(long long x) const {
     const long long big = (base + 1) * rest;
-    return x < big ? (int)(x / (base + 1)) : rest + (int)((x - big) / base);
+    return x < big ? (int)quotient(x, base + 1) : rest + (int)quotient(x - big, base);
   }
 };
 
-// Every thread of the block takes part.  plan.b = batch when the share is empty.
+// A row tile of a sequence and a key/value head; start: where its work begins.
+struct Item {
+  int b, rt, h, q0, n, len, nrt;
+  Span s;
+  long long start;
+};
+
+template <int ROWS>
+__device__ __forceinline__ int load_sequence(const KvAttnArgs& a, int b, Item& it) {
+  bool wrong;
+  lengths_of(a, b, it.q0, it.n, it.len, wrong);
+  it.b = b;
+  it.nrt = (it.n * a.group + ROWS - 1) / ROWS;
+  return wrong;
+}
+
+// The item after `it`; false behind the last.
+template <int ROWS>
+__device__ __forceinline__ bool next_item(const KvAttnArgs& a, Item& it) {
+  it.start += it.s.tiles + kOver;
+  if (++it.h < a.p.heads) return true;
+  it.h = 0;
+  if (++it.rt == it.nrt) {
+    it.rt = 0;
+    do {
+      if (++it.b >= a.batch) return false;
+      load_sequence<ROWS>(a, it.b, it);
+    } while (it.nrt == 0);
+  }
+  it.s = span_of<ROWS>(a, it.n, it.len, it.rt);
+  return true;
+}
+
+// Where a share of the work begins: all of it, the share's first, its item.
+struct Plan {
+  long long total, first;
+  Item it;
+};
+
+// Every thread of the block takes part.  The item is set unless the share is
+// empty.
 template <int ROWS>
 __device__ __forceinline__ void make_plan(const KvAttnArgs& a, int share, int shares, Plan* plan, long long* warp_sum,
                                           bool tell) {
   const int tid = threadIdx.x, per = (a.batch + kThreads - 1) / kThreads;
-  const int b0 = tid * per, b1 = min(a.batch, b0 + per);
+  const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
   long long mine = 0;
   bool bad = false;
+  Item it;
   for (int b = b0; b < b1; ++b) {
-    int q0, n, len;
-    bool wrong;
-    lengths_of(a, b, q0, n, len, wrong);
-    bad |= wrong;
-    mine += tiles_of<ROWS>(a, n, len);
+    bad |= load_sequence<ROWS>(a, b, it);
+    long long tiles = 0;
+    for (int rt = 0; rt < it.nrt; ++rt) tiles += span_of<ROWS>(a, it.n, it.len, rt).tiles + kOver;
+    mine += tiles * a.p.heads;
   }
   if (bad && tell && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
   long long upto = mine;
@@ -254,7 +297,6 @@ __device__ __forceinline__ void make_plan(const KvAttnArgs& a, int share, int sh
     if ((tid & 31) >= o) upto += x;
   }
   if ((tid & 31) == 31) warp_sum[tid >> 5] = upto;
-  if (tid == 0) plan->b = a.batch;
   __syncthreads();
   long long before = 0, total = 0;
   for (int w = 0; w < kWarps; ++w) {
@@ -265,62 +307,30 @@ __device__ __forceinline__ void make_plan(const KvAttnArgs& a, int share, int sh
   const long long first = Split(total, shares).first(share);
   if (tid == 0) { plan->total = total; plan->first = first; }
   if (first >= upto - mine && first < upto) {
-    long long at = upto - mine;
+    long long x = upto - mine;
     for (int b = b0; b < b1; ++b) {
-      int q0, n, len;
-      bool wrong;
-      lengths_of(a, b, q0, n, len, wrong);
-      const long long t = tiles_of<ROWS>(a, n, len);
-      if (first < at + t) {
-        plan->b = b;
-        plan->at = at;
-        break;
+      if (per > 1) load_sequence<ROWS>(a, b, it);
+      for (int rt = 0; rt < it.nrt; ++rt) {
+        it.s = span_of<ROWS>(a, it.n, it.len, rt);
+        const int each = it.s.tiles + kOver;
+        const long long all = (long long)each * a.p.heads;
+        if (first >= x && first < x + all) {
+          it.rt = rt;
+          it.h = (int)quotient(first - x, each);
+          it.start = x + (long long)it.h * each;
+          plan->it = it;
+        }
+        x += all;
       }
-      at += t;
     }
   }
   __syncthreads();
 }
 
-// The item that holds tile `pos`, walking on from sequence b whose first
-// tile is `at`.
-struct Item {
-  int b, rt, h, q0, n, len, nrt;
-  long long at, start;          // first tile of the sequence, of the item
-  Span s;
-};
-
-template <int ROWS>
-__device__ __forceinline__ bool find_item(const KvAttnArgs& a, long long pos, int b, long long at, Item& it) {
-  for (; b < a.batch; ++b) {
-    bool wrong;
-    lengths_of(a, b, it.q0, it.n, it.len, wrong);
-    it.nrt = (it.n * a.group + ROWS - 1) / ROWS;
-    long long x = at;
-    for (int rt = 0; rt < it.nrt; ++rt) {
-      const Span s = span_of<ROWS>(a, it.n, it.len, rt);
-      const long long all = (long long)s.tiles * a.p.heads;
-      if (pos < x + all) {
-        it.b = b;
-        it.rt = rt;
-        it.h = (int)((pos - x) / s.tiles);
-        it.at = at;
-        it.start = x + (long long)it.h * s.tiles;
-        it.s = s;
-        return true;
-      }
-      x += all;
-    }
-    at = x;
-  }
-  return false;
-}
-
 // One row of a finished item: values d .. d + 3 and (lane 0 of the row) lse.
-__device__ __forceinline__ void write_row(const KvAttnArgs& a, const Item& it, int r, int d, int D, float4 o, float M,
+__device__ __forceinline__ void write_row(const KvAttnArgs& a, int h, int t, int hq, int d, int D, float4 o, float M,
                                           float L) {
-  const int i = r / a.group, hq = it.h * a.group + (r - i * a.group), t = it.q0 + i;
-  const float f = L == 0.0f ? 0.0f : __fdividef(a.p.vst[it.h], L);
+  const float f = L == 0.0f ? 0.0f : __fdividef(a.p.vst[h], L);
   const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * f, o.y * f), y = __floats2bfloat162_rn(o.z * f, o.w * f);
   uint2 w;
   w.x = *reinterpret_cast<const uint32_t*>(&x);
@@ -345,22 +355,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   float* stat = reinterpret_cast<float*>(smem + C::kOffStat);
   float* row_rs = reinterpret_cast<float*>(smem + C::kOffRow);
   int *row_hi = reinterpret_cast<int*>(row_rs + R), *row_lo = row_hi + R;
+  int *row_t = row_lo + R, *row_hq = row_t + R;     // -1 for a row that there is not
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffPlan - 16);
   const uint32_t bar_s = sbase + C::kOffBar + 16 * grp, bar_r = bar_s + 8;
   const uint32_t off_k = sbase + grp * C::kGroup, off_v = off_k + kStagesK * C::kTile1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) {
+  static_assert(sizeof(Plan) <= 128, "plan");
+  if (warp == kWarps - 1 && lane == 0) {
     for (int b = 0; b < 4; ++b)   // scores: one commit; ready: an arrival from each warp of the group
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(sbase + C::kOffBar + 8 * b), "r"(b & 1 ? 4 : 1)
                    : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) {
+  if (warp == kWarps - 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_u32(tmem_slot)), "r"(C::kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  make_plan<R>(a, blockIdx.x, gridDim.x, plan, reinterpret_cast<long long*>(smem + C::kOffPlan + 64), blockIdx.x == 0);
+  make_plan<R>(a, blockIdx.x, gridDim.x, plan, reinterpret_cast<long long*>(smem + C::kOffPlan + 128), blockIdx.x == 0);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -373,8 +385,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   }
   const long long first = plan->first, last = Split(plan->total, gridDim.x).first(blockIdx.x + 1);
-  int walk_b = plan->b;
-  long long walk_at = plan->at;
+  Item it = plan->it;
   uint32_t ph_s = 0, ph_r = 0;  // parities of the next scores and of the next keys
   // what a lane reads of a tile's values: tokens c, 4 + (c ^ 1) and both + 8, of 16 (row_token)
   const uint32_t v_at0 = c * (D / 2) + (D / 16) * g, v_at1 = (4 + (c ^ 1)) * (D / 2) + (D / 16) * g;
@@ -387,14 +398,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   const uint32_t ks_at = C::kCodes + 4 * wq + 512 * (lane & (D / 64 - 1)) + (lane / (D / 64)) * 16;
   const uint32_t w_at = 32 * wq * (D / 2) + lane * 16, ws_at = C::kCodes + 32 * wq * (D / 16) + lane * 16;
   bool dead = false;            // a wait gave up
-  for (long long pos = first; pos < last;) {
-    Item it;
-    if (!find_item<R>(a, pos, walk_b, walk_at, it)) break;
-    walk_b = it.b;
-    walk_at = it.at;
-    const int ta = (int)(pos - it.start), tb = (int)min((long long)it.s.tiles, last - it.start);
+  bool more = first < last;
+  for (long long pos = first; more && pos < last; more = next_item<R>(a, it)) {
+    const int ta = (int)max(0ll, pos - it.start - kOver), tb = (int)min((long long)it.s.tiles, last - it.start - kOver);
+    if (tb <= ta) break;         // the share ends before the item's first tile
     const long long seg_pos = pos;
-    pos = it.start + tb;
+    pos = it.start + kOver + it.s.tiles;
     const int h = it.h;
     const int mine = (tb - ta + 1 - grp) / 2;          // this group's tiles: ta + grp + 2 i
     const int32_t* ids_row = a.pages + (long long)it.b * a.max_pages;
@@ -489,15 +498,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       uint32_t digits[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) digits[k] = 0;
+      // n = sum of d_k 8^k with d_k in -4 .. 3 (the last one -4 .. 4): the octal
+      // digits of n + 4 (8^7 - 1) / 7 less 4.  Codes of four values at once:
+      // a permute looks the digits up in a table of bytes.
+      int n[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) n[e] = (sc.finite ? __float2int_rn(v[e] * sc.up1 * sc.up2 * 256.0f) : 0) + 1198372;
+#pragma unroll
+      for (int k = 0; k < 7; ++k) {
+        uint32_t pick = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) pick |= (((uint32_t)n[e] >> (3 * k)) & 7u) << (4 * e);
+        const uint32_t b = __byte_perm(0x090a0b0cu, 0x03020100u, pick);
+        digits[k] = __byte_perm(b | b >> 4, 0u, 0x4420u);
+      }
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        int n = sc.finite ? __float2int_rn(v[e] * sc.up1 * sc.up2 * 256.0f) : 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int d = k < 7 ? ((n + 4) & 7) - 4 : n;
-          n = (n - d) >> 3;
-          digits[k] |= (uint32_t)(d < 0 ? 8 - d : d) << (4 * e);
-        }
+        const int d = n[e] >> 21;
+        digits[7] |= (uint32_t)(d < 0 ? 8 - d : d) << (4 * e);
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -511,6 +529,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         row_rs[r] = sc.finite ? base_scale * sc.down1 * sc.down2 * 0.5f : CUDART_NAN_F;
         row_hi[r] = live ? hi : 0;
         row_lo[r] = live ? query_lo(a, hi) : 0;
+        const int i = live ? row / a.group : 0;
+        row_t[r] = live ? it.q0 + i : -1;
+        row_hq[r] = h * a.group + (row - i * a.group);
       }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -732,16 +753,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     // ---- join the warps' results through shared memory (over the stages: their copies have all landed)
     __syncthreads();
     float* om = reinterpret_cast<float*>(smem);
+    // the sums over the lanes: each step halves the rows that a lane holds
+    float ls[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float t = (r & 1) ? l[r / 2].y : l[r / 2].x;
+      ls[r] = (r & 1) ? l[r / 2].y : l[r / 2].x;
+      if (lane == r) stat[warp * R + r] = kLift - ((r & 1) ? off[r / 2].y : off[r / 2].x);
+    }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
-      if (lane == r) {
-        stat[warp * R + r] = kLift - ((r & 1) ? off[r / 2].y : off[r / 2].x);
-        stat[(kWarps + warp) * R + r] = t;
+    for (int mask = 16, left = R; mask; mask >>= 1) {
+      if (left > 1) {
+        left /= 2;
+#pragma unroll
+        for (int r = 0; r < left; ++r) {
+          const float other = __shfl_xor_sync(~0u, lane & mask ? ls[r] : ls[r + left], mask);
+          ls[r] = (lane & mask ? ls[r + left] : ls[r]) + other;
+        }
+      } else {
+        ls[0] += __shfl_xor_sync(~0u, ls[0], mask);
       }
     }
+    constexpr int kShift = NT == 1 ? 2 : 1;    // lane bits that no row needed
+    if ((lane & ((1 << kShift) - 1)) == 0) stat[(kWarps + warp) * R + (lane >> kShift)] = ls[0];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -766,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
       }
       if (whole) {
-        if (it.rt * R + r < it.n * a.group) write_row(a, it, it.rt * R + r, d, D, o, M, L);
+        if (row_t[r] >= 0) write_row(a, h, row_t[r], row_hq[r], d, D, o, M, L);
       } else {
         float* p = part + (long long)(2 * blockIdx.x + (seg_pos == first ? 0 : 1)) * C::kPart;
         *reinterpret_cast<float4*>(p + r * D + d) = o;
@@ -781,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   if (dead && a.status) atomicOr(a.status, FOS_STATUS_TIMEOUT);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == 0) {
+  if (warp == kWarps - 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(C::kTmemCols) : "memory");
   }
@@ -802,14 +835,14 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttnArgs a, const 
   make_plan<R>(a, blockIdx.x, gridDim.x, &plan, sums, false);
   const Split split(plan.total, gridDim.x);
   const long long first = plan.first, last = split.first(blockIdx.x + 1);
-  Item it;
-  bool mine = first < last && find_item<R>(a, first, plan.b, plan.at, it);
+  const Item it = plan.it;
+  bool mine = first < last;
   int c0 = 0, c1 = 0, lead = 0;
   if (mine) {
-    c0 = split.of(it.start);
-    c1 = split.of(it.start + it.s.tiles - 1);
+    c0 = split.of(it.start + kOver);
+    c1 = split.of(it.start + kOver + it.s.tiles - 1);
     lead = split.first(c0) < it.start ? c0 + 1 : c0;   // the first share that begins with this item or inside it
-    mine = c1 > c0;
+    mine = c1 > c0 && (int)blockIdx.x >= lead;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!mine) return;
@@ -849,7 +882,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttnArgs a, const 
         o.x = o.x * f + v.x * k; o.y = o.y * f + v.y * k; o.z = o.z * f + v.z * k; o.w = o.w * f + v.w * k;
         M = top;
       }
-      write_row(a, it, it.rt * R + r, 4 * lane, D, o, M, L);
+      const int row = it.rt * R + r, i = row / a.group;
+      write_row(a, it.h, it.q0 + i, it.h * a.group + (row - i * a.group), 4 * lane, D, o, M, L);
     }
     __syncthreads();
   }
