@@ -41,7 +41,8 @@ struct Cfg {
   static constexpr int kOffK = kOffQ + 2 * kOperand;
   static constexpr int kOffV = kOffK + 2 * kOperand;
   static constexpr int kOffValid = kOffV + 2 * kOperand;      // visible-token masks, ring of 4 tiles x 128 bits
-  static constexpr int kOffBar = kOffValid + 64;
+  static constexpr int kOffScale = kOffValid + 64;            // the rows' powers of two
+  static constexpr int kOffBar = kOffScale + kRows * 4;
   static constexpr int kBars = 16;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;        // tensor memory base, failure flag, the item
   static constexpr int kSmem = kOffMisc + 256 + 1024;         // + alignment slack
@@ -152,13 +153,12 @@ __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int thr
   const int tid = threadIdx.x, per = (a.batch + threads - 1) / threads;
   const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
   int mine = 0;
-  bool bad = false;
+  bool bad = false, wrong;
+  Item it;
   for (int b = b0; b < b1; ++b) {
-    int q0, n, len;
-    bool wrong;
-    lengths_of(a, b, q0, n, len, wrong);
+    lengths_of(a, b, it.q0, it.n, it.len, wrong);
     bad |= wrong;
-    mine += (int)(((long long)n * a.group + kRows - 1) / kRows);
+    mine += (it.n * a.group + kRows - 1) / kRows;
   }
   if (bad && tell && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
   int upto = mine;
@@ -174,15 +174,13 @@ __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int thr
   int at = upto - mine;
   if (want >= at && want < upto)
     for (int b = b0; b < b1; ++b) {
-      Item it;
-      bool wrong;
-      lengths_of(a, b, it.q0, it.n, it.len, wrong);
-      const int nrt = (int)(((long long)it.n * a.group + kRows - 1) / kRows);
+      if (per > 1) lengths_of(a, b, it.q0, it.n, it.len, wrong);
+      const int nrt = (it.n * a.group + kRows - 1) / kRows;
       if (want < at + nrt) {
         it.b = b;
         it.rt = nrt - 1 - (want - at);
-        const int first = (int)((long long)it.rt * kRows / a.group);
-        const int last = (int)(min((long long)it.n * a.group - 1, (long long)it.rt * kRows + kRows - 1) / a.group);
+        const int first = it.rt * kRows / a.group;
+        const int last = min(it.n * a.group - 1, it.rt * kRows + kRows - 1) / a.group;
         it.hi = query_hi(a, it.n, it.len, last);
         it.lo = query_lo(a, query_hi(a, it.n, it.len, first));
         it.base = it.lo & ~15;
@@ -294,36 +292,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
     const bool live = r < it.n * a.group;
     const int qi = live ? r / a.group : 0, hq = h * a.group + (live ? r - qi * a.group : 0);
     if (t < nt) {
-      // the row's query, scaled by a power of two (and the sign of the
-      // softmax scale, so that larger scores are larger weights)
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)(it.q0 + qi) * a.q_ld + (long long)hq * D);
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        const uint4 w = live ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, max((x[e] & 0x7fffu) << 16, x[e] & 0x7fff0000u));
-      }
-      const RowScale sc = row_scale(top);
+      // the warp's 32 queries, a row for D / 8 lanes at a time, scaled by a
+      // power of two (and the sign of the softmax scale, so that larger scores
+      // are larger weights)
       const float kst = a.scale_log2 * a.p.kst[h];
-      const float up1 = kst < 0.0f ? -sc.up1 : sc.up1;
+      uint8_t* qt = smem + C::kOffQ + t * C::kOperand;
+      float* scales = reinterpret_cast<float*>(smem + C::kOffScale) + t * kTileRows + (warp & 3) * 32;
+      constexpr int kLanes = D / 8, kStep = 32 / kLanes;
+      const int chunk = lane & (kLanes - 1);
+      // all of the warp's loads are on their way before the first is used
+      uint4 qw[kLanes];
+#pragma unroll
+      for (int y = 0; y < kLanes; ++y) {
+        const int rr = min(it.rt * kRows + t * kTileRows + (warp & 3) * 32 + y * kStep + lane / kLanes,
+                           it.n * a.group - 1), i = rr / a.group;
+        qw[y] = __ldg(reinterpret_cast<const uint4*>(a.q + (long long)(it.q0 + i) * a.q_ld +
+                                                     (long long)(h * a.group + (rr - i * a.group)) * D) + chunk);
+      }
+#pragma unroll
+      for (int y8 = 0; y8 < kLanes; ++y8) {
+        const int x = y8 * kStep + lane / kLanes, row = (warp & 3) * 32 + x;
+        uint4 w = qw[y8];
+        if (it.rt * kRows + t * kTileRows + row >= it.n * a.group) w = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t x4[4] = {w.x, w.y, w.z, w.w};
+        uint32_t top = 0, y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max((x4[e] & 0x7fffu) << 16, x4[e] & 0x7fff0000u));
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+        const RowScale sc = row_scale(top);
+        const float up1 = kst < 0.0f ? -sc.up1 : sc.up1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          y[e] = sc.finite ? pack_h2(bf_lo(x4[e]) * up1 * sc.up2, bf_hi(x4[e]) * up1 * sc.up2) : 0u;
+        *reinterpret_cast<uint4*>(qt + (chunk >> 3) * C::kHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+        if (chunk == 0) scales[x] = sc.finite ? fabsf(kst) * sc.down1 * sc.down2 : CUDART_NAN_F;
+      }
+      __syncwarp();
       const int hi = live ? query_hi(a, it.n, it.len, qi) : 0, lo = query_lo(a, hi);
       // never 0 (2^-120 leaves every score's weight at 1), and not NaN for a
       // row without keys: masked scores are -inf before they are scaled
-      float rs = sc.finite ? fabsf(kst) * sc.down1 * sc.down2 : CUDART_NAN_F;
+      float rs = scales[lane];
       if (rs < 7.52316385e-37f || hi <= lo) rs = 7.52316385e-37f;
-      uint8_t* qt = smem + C::kOffQ + t * C::kOperand;
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        const uint4 w = live && sc.finite ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-        uint32_t y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = pack_h2(bf_lo(x[e]) * up1 * sc.up2, bf_hi(x[e]) * up1 * sc.up2);
-        *reinterpret_cast<uint4*>(qt + (k >> 3) * C::kHalf + rl * 128 + (((k & 7) ^ (rl & 7)) << 4)) =
-            make_uint4(y[0], y[1], y[2], y[3]);
-      }
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + 8 * B_Q);
@@ -402,44 +413,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
       }
       if (J > 0 && ok) ok = __all_sync(~0u, mbar_wait(bar + 8 * (B_O + t), 0, fail));
       fence_after();
-      // the output row: a warp's lanes write their rows 64 bytes at a time
+      // the output: a warp's rows through shared memory (its queries', which
+      // no product reads any more), so that whole rows are written at once
       const float msc = m == -CUDART_INF_F ? -CUDART_INF_F : m * rs;
       const bool split = gridDim.y > 1;
       const long long row = (long long)(it.q0 + qi) * a.q_heads + hq;
       const long long all = (long long)a.total_q * a.q_heads;
       const float f = l == 0.0f ? 0.0f : __fdividef(a.p.vst[h], l);
-      if (J > 0 && ok) {
+      const bool none = l == 0.0f || J == 0 || !ok;
+      uint8_t* ot = smem + C::kOffQ + t * C::kOperand + (warp & 3) * 32 * D * 2;
 #pragma unroll 1
-        for (int k = 0; k < D; k += 32) {
-          uint32_t o[32];
+      for (int k = 0; k < D; k += 32) {
+        uint32_t o[32];
+        if (J > 0 && ok) {
           tmem_ld32(to + k, o);
           tmem_wait_ld();
-          if (live && split) {
+        }
+        if (split) {
+          if (live && J > 0) {
             float4* dst = reinterpret_cast<float4*>(part + (blockIdx.y * all + row) * D + k);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                                    __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-          } else if (live) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + (long long)(it.q0 + qi) * a.out_ld + (long long)hq * D + k);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(l == 0.0f ? 0.0f : __uint_as_float(o[8 * e + 2 * i]) * f,
-                                                               l == 0.0f ? 0.0f : __uint_as_float(o[8 * e + 2 * i + 1]) * f);
-                w[i] = *reinterpret_cast<const uint32_t*>(&b);
-              }
-              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
           }
-          __syncwarp();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(none ? 0.0f : __uint_as_float(o[8 * e + 2 * i]) * f,
+                                                             none ? 0.0f : __uint_as_float(o[8 * e + 2 * i + 1]) * f);
+              w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            const int c = k / 8 + e;
+            *reinterpret_cast<uint4*>(ot + lane * D * 2 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
-      } else if (live && !split) {
-        uint4* dst = reinterpret_cast<uint4*>(a.out + (long long)(it.q0 + qi) * a.out_ld + (long long)hq * D);
-#pragma unroll 1
-        for (int k = 0; k < D / 8; ++k) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
+      }
+      if (!split) {
+#pragma unroll 4
+        for (int x = lane / kLanes; x < 32; x += kStep) {
+          const int rr = it.rt * kRows + t * kTileRows + (warp & 3) * 32 + x;
+          if (rr < it.n * a.group) {
+            const int i = rr / a.group;
+            reinterpret_cast<uint4*>(a.out + (long long)(it.q0 + i) * a.out_ld +
+                                     (long long)(h * a.group + (rr - i * a.group)) * D)[chunk] =
+                *reinterpret_cast<const uint4*>(ot + x * D * 2 + ((chunk ^ (x & 7)) << 4));
+          }
+        }
       }
       if (live) {
         if (split) {
