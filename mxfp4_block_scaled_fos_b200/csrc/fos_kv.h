@@ -56,6 +56,7 @@ struct KvAttnArgs {
   const int32_t *cu_q, *pages, *kv_len;
   long long max_pages;
   int total_q, batch, q_heads, group;     // group = q_heads / heads
+  FastDiv by_group;                       // rows are below 2^31
   int causal;
   long long window;                       // 0: none
   float scale_log2;                       // scale * log2(e)

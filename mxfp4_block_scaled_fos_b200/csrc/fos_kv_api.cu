@@ -193,6 +193,7 @@ fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_
   a.batch = (int)batch;
   a.q_heads = (int)q_heads;
   a.group = (int)(q_heads / a.p.heads);
+  a.by_group = make_fastdiv((uint32_t)a.group);
   a.causal = causal;
   a.window = window;
   a.scale_log2 = scale * 1.4426950408889634f;

@@ -200,8 +200,8 @@ __device__ __forceinline__ Span span_of(const KvAttnArgs& a, int n, int len, int
   Span s;
   int first = 0, last = n - 1;
   if (n * a.group > ROWS) {
-    first = rt * ROWS / a.group;
-    last = min(n * a.group - 1, rt * ROWS + ROWS - 1) / a.group;
+    first = fdiv(rt * ROWS, a.by_group);
+    last = fdiv(min(n * a.group - 1, rt * ROWS + ROWS - 1), a.by_group);
   }
   s.hi = query_hi(a, n, len, last);
   s.lo = query_lo(a, query_hi(a, n, len, first));
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = 0.0f;
       if (live) {
-        const int i = row / a.group;
+        const int i = (int)fdiv(row, a.by_group);
         const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + (long long)(it.q0 + i) * a.q_ld +
                                                                 (long long)(h * a.group + (row - i * a.group)) * D) +
                               lane * (E / 2);
@@ -524,12 +524,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
         else *dst = (uint8_t)digits[k];
       }
       if (lane == 0) {
-        const int hi = live ? query_hi(a, it.n, it.len, row / a.group) : 0;
+        const int hi = live ? query_hi(a, it.n, it.len, (int)fdiv(row, a.by_group)) : 0;
         // a digit is twice its E2M1 value, the low set's scale is 2^-6: 2^7; and the 2^8 from above
         row_rs[r] = sc.finite ? base_scale * sc.down1 * sc.down2 * 0.5f : CUDART_NAN_F;
         row_hi[r] = live ? hi : 0;
         row_lo[r] = live ? query_lo(a, hi) : 0;
-        const int i = live ? row / a.group : 0;
+        const int i = live ? (int)fdiv(row, a.by_group) : 0;
         row_t[r] = live ? it.q0 + i : -1;
         row_hq[r] = h * a.group + (row - i * a.group);
       }
@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttnArgs a, const 
         o.x = o.x * f + v.x * k; o.y = o.y * f + v.y * k; o.z = o.z * f + v.z * k; o.w = o.w * f + v.w * k;
         M = top;
       }
-      const int row = it.rt * R + r, i = row / a.group;
+      const int row = it.rt * R + r, i = (int)fdiv(row, a.by_group);
       write_row(a, it.h, it.q0 + i, it.h * a.group + (row - i * a.group), 4 * lane, D, o, M, L);
     }
     __syncthreads();

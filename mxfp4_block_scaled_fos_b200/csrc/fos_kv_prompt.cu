@@ -179,8 +179,8 @@ __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int thr
       if (want < at + nrt) {
         it.b = b;
         it.rt = nrt - 1 - (want - at);
-        const int first = it.rt * kRows / a.group;
-        const int last = min(it.n * a.group - 1, it.rt * kRows + kRows - 1) / a.group;
+        const int first = fdiv(it.rt * kRows, a.by_group);
+        const int last = fdiv(min(it.n * a.group - 1, it.rt * kRows + kRows - 1), a.by_group);
         it.hi = query_hi(a, it.n, it.len, last);
         it.lo = query_lo(a, query_hi(a, it.n, it.len, first));
         it.base = it.lo & ~15;
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
     const int t = warp >> 2, rl = (warp & 3) * 32 + lane;    // tile, row in it
     const int r = it.rt * kRows + t * kTileRows + rl;
     const bool live = r < it.n * a.group;
-    const int qi = live ? r / a.group : 0, hq = h * a.group + (live ? r - qi * a.group : 0);
+    const int qi = live ? (int)fdiv(r, a.by_group) : 0, hq = h * a.group + (live ? r - qi * a.group : 0);
     if (t < nt) {
       // the warp's 32 queries, a row for D / 8 lanes at a time, scaled by a
       // power of two (and the sign of the softmax scale, so that larger scores
@@ -305,26 +305,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
 #pragma unroll
       for (int y = 0; y < kLanes; ++y) {
         const int rr = min(it.rt * kRows + t * kTileRows + (warp & 3) * 32 + y * kStep + lane / kLanes,
-                           it.n * a.group - 1), i = rr / a.group;
+                           it.n * a.group - 1), i = (int)fdiv(rr, a.by_group);
         qw[y] = __ldg(reinterpret_cast<const uint4*>(a.q + (long long)(it.q0 + i) * a.q_ld +
                                                      (long long)(h * a.group + (rr - i * a.group)) * D) + chunk);
       }
+      uint32_t tops[kLanes];
 #pragma unroll
-      for (int y8 = 0; y8 < kLanes; ++y8) {
-        const int x = y8 * kStep + lane / kLanes, row = (warp & 3) * 32 + x;
-        uint4 w = qw[y8];
-        if (it.rt * kRows + t * kTileRows + row >= it.n * a.group) w = make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t x4[4] = {w.x, w.y, w.z, w.w};
-        uint32_t top = 0, y[4];
+      for (int y = 0; y < kLanes; ++y) {
+        const uint32_t x4[4] = {qw[y].x, qw[y].y, qw[y].z, qw[y].w};
+        tops[y] = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, max((x4[e] & 0x7fffu) << 16, x4[e] & 0x7fff0000u));
+        for (int e = 0; e < 4; ++e) tops[y] = max(tops[y], max((x4[e] & 0x7fffu) << 16, x4[e] & 0x7fff0000u));
+      }
 #pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+      for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+        for (int y = 0; y < kLanes; ++y) tops[y] = max(tops[y], __shfl_xor_sync(~0u, tops[y], o));
+#pragma unroll
+      for (int r8 = 0; r8 < kLanes; ++r8) {
+        const int x = r8 * kStep + lane / kLanes, row = (warp & 3) * 32 + x;
+        const bool there = it.rt * kRows + t * kTileRows + row < it.n * a.group;
+        const uint32_t top = tops[r8], x4[4] = {qw[r8].x, qw[r8].y, qw[r8].z, qw[r8].w};
+        uint32_t y[4];
         const RowScale sc = row_scale(top);
         const float up1 = kst < 0.0f ? -sc.up1 : sc.up1;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          y[e] = sc.finite ? pack_h2(bf_lo(x4[e]) * up1 * sc.up2, bf_hi(x4[e]) * up1 * sc.up2) : 0u;
+          y[e] = there && sc.finite ? pack_h2(bf_lo(x4[e]) * up1 * sc.up2, bf_hi(x4[e]) * up1 * sc.up2) : 0u;
         *reinterpret_cast<uint4*>(qt + (chunk >> 3) * C::kHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
             make_uint4(y[0], y[1], y[2], y[3]);
         if (chunk == 0) scales[x] = sc.finite ? fabsf(kst) * sc.down1 * sc.down2 : CUDART_NAN_F;
@@ -454,11 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
         __syncwarp();
       }
       if (!split) {
-#pragma unroll 4
+#pragma unroll
         for (int x = lane / kLanes; x < 32; x += kStep) {
           const int rr = it.rt * kRows + t * kTileRows + (warp & 3) * 32 + x;
           if (rr < it.n * a.group) {
-            const int i = rr / a.group;
+            const int i = (int)fdiv(rr, a.by_group);
             reinterpret_cast<uint4*>(a.out + (long long)(it.q0 + i) * a.out_ld +
                                      (long long)(h * a.group + (rr - i * a.group)) * D)[chunk] =
                 *reinterpret_cast<const uint4*>(ot + x * D * 2 + ((chunk ^ (x & 7)) << 4));
@@ -619,7 +626,7 @@ __global__ void __launch_bounds__(256) k_kv_prompt_join(const KvAttnArgs a, cons
   for (int x = threadIdx.x / kLanes; x < kRows; x += 256 / kLanes) {
     const int r = it.rt * kRows + x;
     if (r >= it.n * a.group) break;
-    const int qi = r / a.group, hq = h * a.group + (r - qi * a.group);
+    const int qi = (int)fdiv(r, a.by_group), hq = h * a.group + (r - qi * a.group);
     const long long row = (long long)(it.q0 + qi) * a.q_heads + hq;
     float M = -CUDART_INF_F, L = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
