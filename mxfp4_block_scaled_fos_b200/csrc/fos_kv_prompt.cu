@@ -609,7 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
   if (tid == 0 && *fail && a.status) atomicOr(a.status, FOS_STATUS_TIMEOUT);
 }
 
-// Adds the results of the CTAs that shared an item's tokens.
+// Adds the results of the CTAs that shared an item's tokens; blockIdx.y: which
+// 256 / (D / 4) of its rows.
 template <int D>
 __global__ void __launch_bounds__(256) k_kv_prompt_join(const KvAttnArgs a, const float* part, int splits) {
   __shared__ Item item;
@@ -623,32 +624,31 @@ __global__ void __launch_bounds__(256) k_kv_prompt_join(const KvAttnArgs a, cons
   const float2* stat = reinterpret_cast<const float2*>(part + (long long)splits * all * D);
   constexpr int kLanes = D / 4;
   const int d = (threadIdx.x % kLanes) * 4;
-  for (int x = threadIdx.x / kLanes; x < kRows; x += 256 / kLanes) {
-    const int r = it.rt * kRows + x;
-    if (r >= it.n * a.group) break;
-    const int qi = (int)fdiv(r, a.by_group), hq = h * a.group + (r - qi * a.group);
-    const long long row = (long long)(it.q0 + qi) * a.q_heads + hq;
-    float M = -CUDART_INF_F, L = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = 0; s < splits; ++s) {
-      const float2 ml = stat[s * all + row];
-      if (ml.y == 0.0f) continue;            // saw nothing: its output was not written
-      const float4 v = *reinterpret_cast<const float4*>(part + (s * all + row) * D + d);
-      const float top = fmaxf(M, ml.x);
-      const float f = M == top ? 1.0f : ex2(M - top), k = ml.x == top ? 1.0f : ex2(ml.x - top);
-      L = L * f + ml.y * k;
-      o.x = o.x * f + v.x * k; o.y = o.y * f + v.y * k; o.z = o.z * f + v.z * k; o.w = o.w * f + v.w * k;
-      M = top;
-    }
-    const float f = L == 0.0f ? 0.0f : __fdividef(a.p.vst[h], L);
-    const __nv_bfloat162 y = __floats2bfloat162_rn(o.x * f, o.y * f), z = __floats2bfloat162_rn(o.z * f, o.w * f);
-    uint2 w;
-    w.x = *reinterpret_cast<const uint32_t*>(&y);
-    w.y = *reinterpret_cast<const uint32_t*>(&z);
-    *reinterpret_cast<uint2*>(a.out + (long long)(it.q0 + qi) * a.out_ld + (long long)hq * D + d) = w;
-    if (d == 0 && a.lse)
-      a.lse[row] = L == 0.0f ? -CUDART_INF_F : (M - kLift + log2f(L)) * 0.69314718055994531f;
+  const int r = it.rt * kRows + blockIdx.y * (256 / kLanes) + threadIdx.x / kLanes;
+  if (r >= it.n * a.group) return;
+  const int qi = (int)fdiv(r, a.by_group), hq = h * a.group + (r - qi * a.group);
+  const long long row = (long long)(it.q0 + qi) * a.q_heads + hq;
+  float M = -CUDART_INF_F, L = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float2 ml = stat[s * all + row];
+    const float4 v = ml.y == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)   // saw nothing: its output was not written
+                                  : *reinterpret_cast<const float4*>(part + (s * all + row) * D + d);
+    const float top = fmaxf(M, ml.x);
+    const float f = M == top ? 1.0f : ex2(M - top), k = ml.x == top ? 1.0f : ex2(ml.x - top);
+    L = L * f + ml.y * k;
+    o.x = o.x * f + v.x * k; o.y = o.y * f + v.y * k; o.z = o.z * f + v.z * k; o.w = o.w * f + v.w * k;
+    M = top;
   }
+  const float f = L == 0.0f ? 0.0f : __fdividef(a.p.vst[h], L);
+  const __nv_bfloat162 y = __floats2bfloat162_rn(o.x * f, o.y * f), z = __floats2bfloat162_rn(o.z * f, o.w * f);
+  uint2 w;
+  w.x = *reinterpret_cast<const uint32_t*>(&y);
+  w.y = *reinterpret_cast<const uint32_t*>(&z);
+  *reinterpret_cast<uint2*>(a.out + (long long)(it.q0 + qi) * a.out_ld + (long long)hq * D + d) = w;
+  if (d == 0 && a.lse)
+    a.lse[row] = L == 0.0f ? -CUDART_INF_F : (M - kLift + log2f(L)) * 0.69314718055994531f;
 }
 
 // Items that the grid has room for: the rows of every sequence in units of 256.
@@ -668,7 +668,7 @@ cudaError_t launch(const KvAttnArgs& a, int splits, float* part, cudaStream_t st
   k_kv_prompt<D><<<dim3((unsigned)grid, splits), kThreads, C::kSmem, st>>>(a, part);
   if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)grid, kRows / (256 / (D / 4)));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
