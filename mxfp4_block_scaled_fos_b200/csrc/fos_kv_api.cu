@@ -54,8 +54,14 @@ fos_status check_rows(const void* x, int64_t ld, int64_t heads, int64_t dim) {
 }
 
 // Which kernel a call of fos_kv_attention runs, from what the host knows.
+// The kernel for few queries reads a sequence's cache again for every 16 rows
+// (queries times heads of a group), the one for many takes 256 at a time but
+// computes 128 whatever there are, and needs more sequences and heads to fill
+// the SMs.  Measured (us, few / many; head_dim 128): batch * heads = 64, 4000
+// tokens: 32 rows 41 / 44, 48 rows 54 / 45; = 256: 16 rows 71 / 142, 48 rows
+// 180 / 142; = 8: 48 rows 18 / 20, 96 rows 25 / 22; = 2: 96 rows 17 / 22.
 struct AttnPlan {
-  bool prompt;
+  bool many;
   int rows, splits;
   size_t bytes;
 };
@@ -63,9 +69,9 @@ struct AttnPlan {
 AttnPlan attn_plan(const fos_kv_cache* c, int64_t total_q, int64_t batch, int64_t q_heads, int64_t max_q,
                    int64_t max_kv) {
   AttnPlan p{};
-  const int64_t group = q_heads / c->heads, rows = max_q * group;
-  p.prompt = rows > 64;
-  if (p.prompt) {
+  const int64_t group = q_heads / c->heads, rows = max_q * group, items = batch * c->heads;
+  p.many = rows > (items >= 32 ? 32 : items >= 8 ? 64 : 128);
+  if (p.many) {
     p.splits = kv_prompt_splits(total_q, batch, group, c->heads, max_kv);
     p.bytes = kv_prompt_workspace_bytes((int)c->head_dim, p.splits, total_q * q_heads);
   } else {
@@ -198,7 +204,7 @@ fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_
   a.window = window;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = status;
-  const cudaError_t ce = plan.prompt ? launch_kv_prompt(a, plan.splits, (float*)workspace, (cudaStream_t)stream)
+  const cudaError_t ce = plan.many ? launch_kv_prompt(a, plan.splits, (float*)workspace, (cudaStream_t)stream)
                                      : launch_kv_decode(a, plan.rows, (float*)workspace, (cudaStream_t)stream);
   return ce == cudaSuccess ? FOS_OK : FOS_ERR_CUDA;
 }
