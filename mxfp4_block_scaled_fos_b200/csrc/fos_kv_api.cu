@@ -55,11 +55,15 @@ fos_status check_rows(const void* x, int64_t ld, int64_t heads, int64_t dim) {
 
 // Which kernel a call of fos_kv_attention runs, from what the host knows.
 // The kernel for few queries reads a sequence's cache again for every 16 rows
-// (queries times heads of a group), the one for many takes 256 at a time but
-// computes 128 whatever there are, and needs more sequences and heads to fill
-// the SMs.  Measured (us, few / many; head_dim 128): batch * heads = 64, 4000
-// tokens: 32 rows 41 / 44, 48 rows 54 / 45; = 256: 16 rows 71 / 142, 48 rows
-// 180 / 142; = 8: 48 rows 18 / 20, 96 rows 25 / 22; = 2: 96 rows 17 / 22.
+// (queries times heads of a group) but cuts the tokens as finely as it takes
+// to fill the SMs; the one for many takes 256 rows at a time, computes 128
+// whatever there are, and gives each CTA 512 tokens at least.  Measured (us,
+// few / many; head_dim 128) by sequences times heads, on each side of the rule:
+//     2, 4000 tokens: 128 rows 18 / 23, 256 rows 21 / 30; 16000: 256 rows 39 / 40
+//     8, 4000 tokens: 64 rows 20 / 21, 96 rows 25 / 22; 16000: 37 / 35, 49 / 36
+//    16, 4000 tokens: 32 rows 20 / 23, 64 rows 28 / 26; 500: 15 / 17, 16 / 17
+//    64, 4000 tokens: 32 rows 41 / 44, 48 rows 54 / 45; 500: 20 / 18, 26 / 18
+//   256, 4000 tokens: 32 rows 126 / 141, 48 rows 180 / 142; 500: 43 / 35, 59 / 36
 struct AttnPlan {
   bool many;
   int rows, splits;
@@ -70,9 +74,9 @@ AttnPlan attn_plan(const fos_kv_cache* c, int64_t total_q, int64_t batch, int64_
                    int64_t max_kv) {
   AttnPlan p{};
   const int64_t group = q_heads / c->heads, rows = max_q * group, items = batch * c->heads;
-  p.many = rows > (items >= 32 ? 32 : items >= 8 ? 64 : 128);
+  p.many = rows > 32 && rows > 512 / (items > 0 ? items : 1);
   if (p.many) {
-    p.splits = kv_prompt_splits(total_q, batch, group, c->heads, max_kv);
+    p.splits = kv_prompt_splits(total_q, batch, group, c->heads, max_q, max_kv);
     p.bytes = kv_prompt_workspace_bytes((int)c->head_dim, p.splits, total_q * q_heads);
   } else {
     p.rows = rows > 16 ? 16 : (int)rows;
@@ -155,7 +159,9 @@ fos_status fos_kv_read(const fos_kv_cache* cache, const int64_t* slots, int64_t 
 
 size_t fos_kv_attention_workspace_size(const fos_kv_cache* cache, int64_t total_q, int64_t batch, int64_t q_heads,
                                        int64_t max_q, int64_t max_pages) {
-  if (!cache || cache->heads < 1 || q_heads < cache->heads || total_q < 1 || batch < 1 || max_q < 0 || max_pages < 0)
+  if (!cache || cache->heads < 1 || q_heads < cache->heads || q_heads > 65536 || total_q < 1 || total_q > (1 << 30) ||
+      batch < 1 || batch > (1 << 20) || max_q < 0 || max_q > (1 << 30) || max_pages < 0 ||
+      max_pages > (1ll << 31) || cache->page_size < 1 || cache->page_size > 128)
     return 0;
   return attn_plan(cache, total_q, batch, q_heads, max_q, max_pages * cache->page_size).bytes;
 }
@@ -205,7 +211,7 @@ fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = status;
   const cudaError_t ce = plan.many ? launch_kv_prompt(a, plan.splits, (float*)workspace, (cudaStream_t)stream)
-                                     : launch_kv_decode(a, plan.rows, (float*)workspace, (cudaStream_t)stream);
+                                   : launch_kv_decode(a, plan.rows, (float*)workspace, (cudaStream_t)stream);
   return ce == cudaSuccess ? FOS_OK : FOS_ERR_CUDA;
 }
 

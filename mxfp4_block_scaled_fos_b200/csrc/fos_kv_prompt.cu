@@ -682,9 +682,12 @@ cudaError_t launch(const KvAttnArgs& a, int splits, float* part, cudaStream_t st
 }  // namespace
 
 // CTAs that share an item's tokens: enough to fill 148 SMs when the items do
-// not, with four tiles of tokens for each at least.
-int kv_prompt_splits(long long total_q, long long batch, long long group, long long heads, long long max_kv) {
-  const long long items = item_bound(total_q, batch, group) * heads;
+// not, with four tiles of tokens for each at least.  max_q bounds the items more
+// tightly than the grid does, which must hold whatever the offsets say.
+int kv_prompt_splits(long long total_q, long long batch, long long group, long long heads, long long max_q,
+                     long long max_kv) {
+  const long long each = batch * ((max_q * group + kRows - 1) / kRows), all = item_bound(total_q, batch, group);
+  const long long items = (each < all ? each : all) * heads;
   const long long tiles = (max_kv + kTileTok - 1) / kTileTok;
   long long s = items >= 148 ? 1 : 148 / items;
   if (s > tiles / 4) s = tiles / 4;
