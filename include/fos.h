@@ -428,8 +428,12 @@ fos_status fos_kv_read(const fos_kv_cache* cache, const int64_t* slots, int64_t 
  * such lengths are clamped.
  *   workspace: fos_kv_attention_workspace_size(...) bytes, 16-byte aligned,
  *           not initialised, not shared by calls that overlap on the GPU.
- * Arithmetic: products of queries and cached values are exact, sums are
- * binary32, the softmax weights are rounded to f16 before the second product.
+ * Arithmetic: a query is held to 2^-23 of its largest |value| or better, its
+ * products with cached keys are exact, sums are binary32, the softmax weights
+ * are rounded to f16 before the second product.  A key whose score is below
+ * -6e29 weighs nothing.  A cached NaN scale (kv_append writes none without
+ * FOS_STATUS_NONFINITE) at a position that one query of a sequence sees may
+ * reach the sequence's other queries; elsewhere the cache may hold anything.
  * The work is split by the lengths alone: the same call gives the same bits.
  */
 size_t fos_kv_attention_workspace_size(const fos_kv_cache* cache, int64_t total_q, int64_t batch, int64_t q_heads,

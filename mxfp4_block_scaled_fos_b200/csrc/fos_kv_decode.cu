@@ -16,24 +16,32 @@
 // 32 tokens of a tile.
 //   S^T = K Q^T runs on the FP4 tensor cores (tcgen05 kind::mxf4nvf4) on the
 // codes and scales as the cache holds them: the 128 tokens are the rows of A.
-// Queries become FP4 operands without loss that counts: a row is scaled by a
-// power of two to integers below 2^23 (24 bits below the row's largest
-// value), written in balanced base 8, and the digits -4 .. 4 are E2M1 values
-// (halves). Digit j and digit j + 4 share column j of a row, as two products
-// with scales 2^-6 and 2^6; a score is the sum of its 4 columns times 8^j.
-// Nothing of a key is converted in registers, where the conversion bounded an
-// earlier version: e2m1 conversions run at 16 values pairs a cycle.
+// Queries become FP4 operands: a row is scaled by a power of two so that its
+// largest value lies in [2^22, 2^23), rounded to integers (off by half a unit,
+// 2^-23 of the row's largest value at most; a bf16 within 2^15 of it is exact),
+// written in balanced base 8, and the digits -4 .. 4 are E2M1 values (halves).
+// Digit j and digit j + 4 share column j of a row, as two products with scales
+// 2^-6 and 2^6; a score is the sum of its 4 columns times 8^j.  So no key is
+// converted in registers, where four codes take a conversion and a product each
+// pair: that is left to the values, a third of the instructions of a tile.
 //   O^T += V^T P^T runs on m16n8k16 with f16 operands: A = 16 output values
 // of 16 tokens, B = the weights of 8 rows. A code times its E4M3 scale has 6
 // significant bits between 2^-10 and 2688, exact in f16. A register holds one
 // value of two tokens: nibbles of two tokens' words are zipped into bytes and
 // converted together (cvt f16x2.e2m1x2). A warp reads the scores of its own
-// tokens, a token for each lane, and only its own values, so warps of a group
-// meet once a tile: to hand over the next tile's key scales and to know that
-// the scores have been read.
+// tokens, a token for each lane, and only its own values, so the warps of a group
+// meet at one barrier a tile, which only the warp that issues the next
+// products waits for: the next tile's keys are there, this one's scores read.
 // The next tile's scores are computed while this one's values are.
 // The running maximum of a row is raised, and its sums rescaled, only when a
 // score passes it by 2^8 (fos_kv.cuh).
+//
+// Measured: 64 sequences of up to 16384 tokens (598 MB of 8 heads of 128,
+// pages of 16) 149 us with k_kv_join, 0.62 of the copy bandwidth; 4 of up to
+// 131072 tokens (407 MB) 102 us, 0.62; one of 1000 tokens 11 us.  A CTA in the
+// middle of a long item reads at 0.95 of it; beginning an item costs it 5 to
+// 7 us (page ids, digits, the first scores, the warps' results joined), which
+// the other CTA of the SM covers in part, and the plan 2 us.
 #include <math_constants.h>
 
 #include "fos_kv.cuh"
@@ -820,7 +828,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   }
 }
 
-// Joins an item that several shares hold: the CTAs of those shares (but one
+// Joins an item that several shares hold (3 us for one of 1000 tokens, begun
+// before k_kv_decode has ended so that its plan costs nothing): the CTAs of those shares (but one
 // that the item only ends) take its rows in turn.  The warps of a CTA take a
 // row each, or several share a row's partial results; every sum is in the
 // order of the tokens within a warp and over the warps in theirs.

@@ -19,6 +19,7 @@ Six", introduction (the adaptive block scale).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple, Union
 
@@ -138,6 +139,10 @@ def _call(cache: "KVCache", what: str, fn, stream, args) -> None:
         raise fos.FosError(st, what)
 
 
+def _empty_like(x: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
 def _rows(name: str, x: torch.Tensor, tokens: int, heads: int, cache: "KVCache") -> int:
     """Checks x as rows of heads; the distance between tokens in elements."""
     if x.dtype is not torch.bfloat16 or x.get_device() != cache._dev:
@@ -202,7 +207,7 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
         hq = q.shape[1]
         q_ld = _rows("q", q, t, hq, cache)
         if q_out is None:
-            q_out, out_ld = q.new_empty((t, hq, cache.head_dim)), hq * cache.head_dim
+            q_out, out_ld = _empty_like(q), hq * cache.head_dim
         else:
             out_ld = _rows("q_out", q_out, t, hq, cache)
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
@@ -233,10 +238,17 @@ def kv_read(cache: KVCache, slots: torch.Tensor, out: Optional[Tuple[torch.Tenso
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(heads: int, head_dim: int, page_size: int, total_q: int, batch: int, q_heads: int, max_q: int,
+                     max_pages: int) -> int:
+    c = _CacheC(heads=heads, head_dim=head_dim, page_size=page_size)
+    return int(_lib().fos_kv_attention_workspace_size(ctypes.byref(c), total_q, batch, q_heads, max_q, max_pages))
+
+
 def kv_attention_workspace_size(cache: KVCache, total_q: int, batch: int, q_heads: int, max_q: int,
                                 max_pages: int) -> int:
     """Bytes of workspace kv_attention needs."""
-    return int(_lib().fos_kv_attention_workspace_size(cache._ref, total_q, batch, q_heads, max_q, max_pages))
+    return _workspace_bytes(cache.heads, cache.head_dim, cache.page_size, total_q, batch, q_heads, max_q, max_pages)
 
 
 def kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, pages: torch.Tensor, kv_len: torch.Tensor,
@@ -266,7 +278,7 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, pages: tor
     cu, table = _ints("cu_q", cu_q, torch.int32, (b + 1,), cache), _ints("pages", pages, torch.int32, (b, most), cache)
     lens = _ints("kv_len", kv_len, torch.int32, (b,), cache)
     if out is None:
-        out, out_ld = q.new_empty((t, hq, cache.head_dim)), hq * cache.head_dim
+        out, out_ld = _empty_like(q), hq * cache.head_dim
     else:
         out_ld = _rows("out", out, t, hq, cache)
     lse_ptr = None
@@ -276,7 +288,7 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, pages: tor
         lse = q.new_empty((t, hq), dtype=torch.float32)
         lse_ptr = lse.data_ptr()
     L = _lib()
-    need = L.fos_kv_attention_workspace_size(cache._ref, t, b, hq, max_q, most)
+    need = _workspace_bytes(cache.heads, cache.head_dim, cache.page_size, t, b, hq, max_q, most)
     if workspace is None and need:
         workspace = q.new_empty((need,), dtype=torch.uint8)
         if stream is not None:

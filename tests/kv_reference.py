@@ -48,9 +48,10 @@ def attention(q, kc, ks, vc, vs, kst, vst, cu, pages, kv_len, causal, window, sc
 
     With n keys, e = 2^-24: a score sums D products (any order: D e times the
     sum of their magnitudes) and takes a few more roundings, and a query may
-    be held to 24 bits below its largest value, so a score is off by ds <=
-    e |scale St| ((D + 8) sum |q k| + max |q| sum |k|); its exponential by 2 ds (score and maximum) + 2^-21 (exp2 and the reduced
-    argument); a weight is rounded to f16 (2^-11, or 2^-25 of the largest
+    be rounded to integers with its largest value in [2^22, 2^23), off by
+    1/2 <= 2^-23 max |q| = 2 e max |q|, so a score is off by ds <=
+    e |scale St| ((D + 8) sum |q k| + 2 max |q| sum |k|); its exponential by
+    2 ds (score and maximum) + 2^-21 (exp2 and the reduced argument); a weight is rounded to f16 (2^-11, or 2^-25 of the largest
     where it is subnormal); the sums over n keys add n e.  The result is
     rounded to bf16 (2^-8)."""
     q = q.double().numpy()
@@ -82,7 +83,7 @@ def attention(q, kc, ks, vc, vs, kst, vst, cu, pages, kv_len, causal, window, sc
                 t = cu[b] + i
                 out[t, h] = p @ v
                 lse[t, h] = top + np.log(total)
-                ds = ((D + 8) * (np.abs(k) @ np.abs(q[t, h])) + np.abs(q[t, h]).max() * np.abs(k).sum(1)).max()
+                ds = ((D + 8) * (np.abs(k) @ np.abs(q[t, h])) + 2 * np.abs(q[t, h]).max() * np.abs(k).sum(1)).max()
                 ds *= 2.0 ** -24 * abs(scale)
                 rel = 2 * ds + 2.0 ** -21 + (hi - lo) * 2.0 ** -23
                 mag = p @ np.abs(v)

@@ -438,3 +438,210 @@ def test_one_key_gives_its_values_for_every_code(dim, max_q):
     got = F.kv_attention(cache, q, torch.arange(n + 1, dtype=I32, device=dev), pages, kv_len, max_q, window=1)
     want = F.kv_read(cache, slots)[1].repeat_interleave(2, 1)
     assert torch.equal(got, want)
+
+
+# both kernels, whatever sizes would choose: max_q is a hint (a small one takes the kernel for few queries)
+@pytest.mark.parametrize("max_q", [1, 1 << 20])
+@pytest.mark.parametrize("dim,page,heads,group,q_len,kv_len,window,causal,gap", [
+    (128, 16, 1, 4, [70, 1, 64], [130, 40, 200], 0, True, 1),
+    (64, 64, 2, 1, [200, 3], [200, 700], 0, True, 3),
+    (128, 32, 1, 3, [45, 97], [333, 97], 50, True, 0),
+    (64, 16, 1, 5, [77, 0, 31], [256, 10, 31], 0, True, 0),
+    (64, 128, 2, 2, [40, 70, 33], [129, 0, 500], 0, False, 1),
+    (128, 64, 1, 2, [257], [255], 0, True, 0),
+    (64, 32, 1, 8, [60, 17], [30, 0], 0, True, 2),
+    (128, 64, 1, 2, [70, 3, 40], [2300, 5, 0], 0, True, 0),
+    (64, 16, 1, 3, [100], [1700], 600, True, 1),
+    (128, 128, 1, 1, [90, 66], [1290, 700], 0, False, 0),
+    (128, 16, 2, 1, [1, 129, 1], [1, 129, 2], 1, True, 0),
+])
+def test_attention_by_either_kernel(dim, page, heads, group, q_len, kv_len, window, causal, gap, max_q):
+    pages, n = _paged(kv_len, page, 14)
+    cache, ref = _random_cache(n, page, heads, dim, 16, gap=gap)
+    cu = [0] + np.cumsum(q_len).tolist()
+    _check(cache, ref, _queries(cu[-1], heads * group, dim, 18, 2.0), cu, pages, kv_len, window=window, causal=causal,
+           max_q=max_q)
+
+
+@pytest.mark.parametrize("max_q", [1, 1 << 20])
+def test_pages_far_apart(max_q):
+    """Pools whose pages lie 2^32 - 16 bytes apart: offsets past 32 bits in all three operators."""
+    dev = require_gpu()
+    stride, n, page, heads, dim = (1 << 32) - 16, 3, 16, 2, 64
+    whole = torch.empty(2 * stride + (1 << 20), dtype=torch.uint8, device=dev)
+    pools = [torch.as_strided(whole, (n, heads, page, dim // d), (stride, page * dim // d, dim // d, 1), at << 14)
+             for at, d in enumerate((2, 16, 2, 16))]
+    st = torch.full((heads,), 5.0 / 1792.0, device=dev)
+    far = F.KVCache(*pools, st, st)
+    near = F.KVCache.empty(n, page, heads, dim, 5.0, 5.0, device=dev)
+    near.k_tensor_scale.copy_(st)
+    near.v_tensor_scale.copy_(st)
+    g = torch.Generator().manual_seed(70)
+    x = torch.randn(n * page, 2 * heads, dim, generator=g).to(torch.bfloat16).to(dev)
+    slots = torch.arange(n * page, device=dev)
+    for c in (far, near):
+        F.kv_append(c, x[:, :heads], x[:, heads:], slots)
+    for a, b in zip(F.kv_read(far, slots), F.kv_read(near, slots)):
+        assert torch.equal(a, b)
+    q = _queries(9, 4, dim, 71).to(dev)
+    args = (q, torch.tensor([0, 2, 9], dtype=I32, device=dev),
+            torch.tensor([[2, 0, 1], [1, 2, -1]], dtype=I32, device=dev), torch.tensor([47, 32], dtype=I32, device=dev),
+            max_q)
+    assert torch.equal(F.kv_attention(far, *args), F.kv_attention(near, *args))
+
+
+@pytest.mark.parametrize("max_q", [1, 1 << 20])
+def test_many_sequences(max_q):
+    """More sequences than a block has threads, some empty: a bundle of single
+    tokens equals the same sequences one at a time."""
+    dev = require_gpu()
+    B, page, dim = 611, 16, 64
+    rng = np.random.RandomState(80)
+    q_len = rng.randint(0, 3, B)
+    kv_len = [int(m) for m in rng.randint(0, 60, B)]
+    kv_len[7] = 400
+    cache, _ = _random_cache(40, page, 1, dim, 81)
+    pages = rng.randint(0, 40, (B, 25)).astype(np.int32)     # pages shared by sequences
+    cu = np.concatenate(([0], np.cumsum(q_len))).astype(np.int32)
+    q = _queries(int(cu[-1]), 2, dim, 82).to(dev)
+    pd, ld = torch.from_numpy(pages).to(dev), torch.tensor(kv_len, dtype=I32, device=dev)
+    got, lse = F.kv_attention(cache, q, torch.from_numpy(cu).to(dev), pd, ld, max_q, return_lse=True)
+    for b in list(range(0, B, 37)) + [7, B - 1]:
+        if not q_len[b]:
+            continue
+        s = slice(int(cu[b]), int(cu[b + 1]))
+        one, l1 = F.kv_attention(cache, q[s], torch.tensor([0, q_len[b]], dtype=I32, device=dev), pd[b:b + 1],
+                                 ld[b:b + 1], 1, return_lse=True)
+        # either answer is within 2^-8 of the other's bf16 and the weights' 2^-11 (values below 6)
+        assert torch.allclose(got[s].float(), one.float(), rtol=2.0 ** -7, atol=6 * 2.0 ** -9), b
+        assert torch.allclose(lse[s], l1, rtol=1e-5, atol=1e-4, equal_nan=True), b
+
+
+@pytest.mark.parametrize("max_q", [1, 1 << 20])
+def test_pages_before_a_window_are_not_read(max_q):
+    dev = require_gpu()
+    kv_len, n_q, window = [500], 6, 40
+    pages, n = _paged(kv_len, 16, 90)
+    cache, ref = _random_cache(n, 16, 1, 128, 91)
+    q = _queries(n_q, 2, 128, 92)
+    want, _ = _check(cache, ref, q, [0, n_q], pages, kv_len, window=window, max_q=max_q)
+    gone = pages.copy()
+    gone[0, :(500 - n_q + 1 - window) // 16] = 1 << 30       # would set the status
+    status = torch.zeros(1, dtype=I32, device=dev)
+    got = F.kv_attention(cache, q.to(dev), torch.tensor([0, n_q], dtype=I32, device=dev),
+                         torch.from_numpy(gone).to(dev), torch.tensor(kv_len, dtype=I32, device=dev), max_q,
+                         window=window, status=status)
+    assert int(status) == 0 and np.array_equal(got.cpu().double().numpy(), want)
+
+
+def test_calls_at_once_and_graphs_of_both_kernels():
+    """Both kernels, with workspaces of their own, on two streams at once; and
+    each captured, the graphs replayed in turn and at once."""
+    dev = require_gpu()
+    kv_len = [3000, 17, 900]
+    pages, n = _paged(kv_len, 64, 100)
+    cache, _ = _random_cache(n, 64, 2, 128, 101)
+    pd, ld = torch.from_numpy(pages).to(dev), torch.tensor(kv_len, dtype=I32, device=dev)
+    calls = []
+    for each, seed in ((1, 102), (90, 103)):
+        q = _queries(3 * each, 8, 128, seed).to(dev)
+        cu = torch.arange(4, dtype=I32, device=dev) * each
+        assert F.kv_attention_workspace_size(cache, 3 * each, 3, 8, each, pages.shape[1]) > 0
+        calls.append(lambda q=q, cu=cu, each=each: F.kv_attention(cache, q, cu, pd, ld, each, return_lse=True))
+    want = [f() for f in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = []
+    for _ in range(4):
+        for s, f in zip(streams, calls):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(f())
+    torch.cuda.synchronize()
+    for i, (y, l) in enumerate(got):
+        assert torch.equal(y, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+    graphs, outs = [], []
+    for f in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(f())
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1)):
+        for y, l in outs:
+            y.zero_()
+            l.zero_()
+        torch.cuda.synchronize()
+        for k, i in enumerate(order):
+            with torch.cuda.stream(streams[k if order[0] != order[1] else 0]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in set(order):
+            assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+
+
+def test_prompt_graph_follows_new_lengths():
+    """A captured call of many queries serves other lengths and pages of the same shapes."""
+    dev = require_gpu()
+    cache, ref = _random_cache(40, 16, 1, 64, 110)
+    cu = torch.tensor([0, 100, 130], dtype=I32, device=dev)
+    pages, lens = torch.zeros(2, 40, dtype=I32, device=dev), torch.zeros(2, dtype=I32, device=dev)
+    q = _queries(130, 4, 64, 111)
+    qd = q.to(dev)
+    F.kv_attention(cache, qd, cu, pages, lens, 1 << 20)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = F.kv_attention(cache, qd, cu, pages, lens, 1 << 20)
+    for seed, n_cu, n_len in ((1, [0, 100, 130], [600, 30]), (2, [0, 30, 130], [10, 639]), (3, [0, 0, 130], [5, 200])):
+        order = np.random.RandomState(seed).permutation(40).astype(np.int32)
+        table = np.stack((order, order[::-1]))
+        cu.copy_(torch.tensor(n_cu, dtype=I32))
+        pages.copy_(torch.from_numpy(table.copy()))
+        lens.copy_(torch.tensor(n_len, dtype=I32))
+        g.replay()
+        want, _, bound, _ = R.attention(q, ref["kc"], ref["ks"], ref["vc"], ref["vs"], ref["kst"], ref["vst"], n_cu,
+                                        table, n_len, True, 0, 1 / 8)
+        assert (np.abs(out.cpu().double().numpy() - want) <= bound).all()
+
+
+def test_binding_refusals():
+    dev = require_gpu()
+    c = F.KVCache.empty(4, 16, 2, 64, 1.0, 1.0, device=dev)
+    bf = dict(dtype=torch.bfloat16, device=dev)
+    k, slots = torch.zeros(3, 2, 64, **bf), torch.arange(3, device=dev)
+    table, pos = _table(9, 64).to(dev), torch.zeros(3, dtype=I32, device=dev)
+    append = lambda *a, **kw: F.kv_append(c, *a, **kw)  # noqa: E731
+    for bad in ((k.float(), k, slots), (k.cpu(), k, slots), (k, k, slots.int()), (k, k, slots.cpu())):
+        with pytest.raises(TypeError):
+            append(*bad)
+    for bad in ((k[:2], k, slots), (k, k, slots[:2]), (k[:, :1], k, slots), (k[..., :32], k, slots),
+                (k.transpose(0, 1).contiguous().transpose(0, 1), k, slots)):
+        with pytest.raises(ValueError):
+            append(*bad)
+    for kw in (dict(cos_sin=table), dict(positions=pos), dict(q=k), dict(q_out=k),
+               dict(cos_sin=table, positions=pos[:2]), dict(cos_sin=table[0], positions=pos)):
+        with pytest.raises(ValueError):
+            append(k, k, slots, **kw)
+    with pytest.raises(TypeError):
+        append(k, k, slots, cos_sin=table.double(), positions=pos)
+    with pytest.raises(F.FosError):
+        append(k, k, slots, cos_sin=_table(9, 24).to(dev), positions=pos)
+    with pytest.raises(TypeError):
+        append(k, k, slots, status=torch.zeros(1, device=dev))
+    q, cu = torch.zeros(3, 4, 64, **bf), torch.tensor([0, 3], dtype=I32, device=dev)
+    pages, lens = torch.zeros(1, 2, dtype=I32, device=dev), torch.ones(1, dtype=I32, device=dev)
+    att = lambda q=q, cu=cu, pages=pages, lens=lens, n=3, **kw: F.kv_attention(c, q, cu, pages, lens, n, **kw)  # noqa: E731
+    att()
+    for kw in (dict(q=q.half()), dict(cu=cu.long()), dict(pages=pages.long()), dict(lens=lens.float()),
+               dict(lse=torch.zeros(3, 4, **bf))):
+        with pytest.raises(TypeError):
+            att(**kw)
+    for kw in (dict(q=q[:, :3]), dict(q=q[0]), dict(pages=pages[0]), dict(lens=lens.expand(2)), dict(window=-1),
+               dict(window=5, causal=False), dict(out=q[:2]), dict(cu=cu[:0])):
+        with pytest.raises(ValueError):
+            att(**kw)
+    for kw in (dict(n=-1), dict(scale=math.nan), dict(workspace=torch.zeros(16, dtype=torch.uint8, device=dev))):
+        with pytest.raises(F.FosError):
+            att(**kw)
+    with pytest.raises(ValueError):
+        F.kv_read(c, slots, out=(k[:2], k))
+    with pytest.raises(TypeError):
+        F.kv_read(c, slots.int())
