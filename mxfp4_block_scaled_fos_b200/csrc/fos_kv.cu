@@ -8,6 +8,7 @@ namespace fos {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kAppendWarps = 24;    // of k_kv_append on an SM: 80 registers, 6 warps on each quarter
 
 // One 16-value block (8 bf16x2 words) -> codes and scale byte by the
 // quantizer's rule with S_t = ts.St.  Pools have one S_t for each head, so
@@ -84,91 +85,105 @@ __device__ __forceinline__ void load32(const uint16_t* p, uint4 (&w)[2]) {
 // first values and the block of their partners rot/2 further on, so that
 // every value is loaded and widened once and an angle serves two of them;
 // otherwise they are neighbours.  Products are fma(x, c, -0) in pairs: rounded
-// by themselves (see the f32x2 helpers), two to an instruction.
+// by themselves (see the f32x2 helpers), two to an instruction.  A CTA has the
+// same rows (every gridDim.y-th) of token after token and loads the next
+// token's while it works on one.
 // Memory-bound for long prompts, where the queries are most of the bytes:
-// 16384 tokens of 32 + 8 + 8 heads of 128 appended and read back (449 MB) 108
-// us, 0.65 of the copy bandwidth; 143 with one block a thread, whose partners
-// are loaded again.  Launch and latency for a decoding step.
+// 16384 tokens of 32 + 8 + 8 heads of 128 appended (363 MB) 75 us, 0.75 of
+// the copy bandwidth; 95 with a token for each CTA (8192 of 64 + 8 + 8 heads 73
+// and 77, 16384 of 8 + 8 + 8 heads of 64 46 and 42); one block a thread, whose
+// partners are loaded again, took 35 more.  Launch and latency for a decoding
+// step.
 // WIDE: all rows 32-byte aligned, one load and one store a block.
 template <bool F46, bool INTER, bool WIDE>
-__global__ void __launch_bounds__(256, 4) k_kv_append(const KvAppendArgs a) {
+__global__ void __launch_bounds__(256, 3) k_kv_append(const KvAppendArgs a) {
   const int lanes = a.p.dim >> 5;
-  const int x = blockIdx.y * blockDim.x + threadIdx.x;
-  const int r = x / lanes, p = x & (lanes - 1);
-  const int t = blockIdx.x;
+  const int r = threadIdx.x / lanes * gridDim.y + blockIdx.y, p = threadIdx.x & (lanes - 1);
+  const bool teller = threadIdx.x == 0 && blockIdx.y == 0;
   const int kind = r < a.q_heads ? 0 : r < a.q_heads + a.p.heads ? 1 : r < a.q_heads + 2 * a.p.heads ? 2 : 3;
   const int h = kind == 0 ? r : kind == 1 ? r - a.q_heads : r - a.q_heads - a.p.heads;
   const int half = a.rot >> 1;
   const bool turned = a.table && kind < 2 && 32 * p < a.rot;
   const int d0 = !INTER && 32 * p < a.rot ? 16 * p : 32 * p;             // the blocks' first values
   const int d1 = !INTER && 32 * p < a.rot ? d0 + half : d0 + 16;
-  uint4 w[2][2];
-  const uint16_t* src = nullptr;
-  if (kind < 3) {
-    src = kind == 0 ? a.q + (long long)t * a.q_ld
-                    : kind == 1 ? a.k + (long long)t * a.k_ld : a.v + (long long)t * a.v_ld;
-    src += h * a.p.dim;
-    load32<WIDE>(src + d0, w[0]);
-    load32<WIDE>(src + d1, w[1]);
-  }
-  const long long slot = a.slots[t];
-  const long long page = slot >> a.p.page_shift;
-  bool write = slot >= 0, turn_ok = true;
-  if (write && page >= a.p.num_pages) {
-    write = false;
-    if (x == 0 && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
-  }
-  if (a.table) {
-    const int pos = a.positions[t];
-    if (pos < 0 || pos >= a.max_positions) {
-      if (x == 0 && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
-      write = turn_ok = false;
-    } else if (turned) {
-      const float* row = a.table + (long long)pos * a.rot;
-      const float2 nz = make_float2(a.neg_zero, a.neg_zero);
-      uint32_t(&W)[2][8] = reinterpret_cast<uint32_t(&)[2][8]>(w);
+  const uint16_t* base = (kind == 0 ? a.q : kind == 1 ? a.k : a.v) + h * a.p.dim;
+  const long long ld = kind == 0 ? a.q_ld : kind == 1 ? a.k_ld : a.v_ld;
+  uint4 w[2][2], w_next[2][2];
+  long long slot_next = 0;
+  int pos_next = 0;
+  auto fetch = [&](int t) {      // what token t brings
+    if (kind < 3) {
+      load32<WIDE>(base + t * ld + d0, w_next[0]);
+      load32<WIDE>(base + t * ld + d1, w_next[1]);
+    }
+    slot_next = __ldg(reinterpret_cast<const long long*>(a.slots) + t);
+    if (a.table) pos_next = __ldg(a.positions + t);
+  };
+  fetch(blockIdx.x);
+#pragma unroll 1
+  for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {       // four pairs of each of two words of either block (INTER: of one word)
-        const int i = INTER ? (d0 >> 1) + 4 * q : d0 + 4 * q;
-        if (INTER && 2 * i >= a.rot) continue;
-        const float4 c = __ldg(reinterpret_cast<const float4*>(row + i));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + i));
+    for (int i = 0; i < 4; ++i) w[i >> 1][i & 1] = w_next[i >> 1][i & 1];
+    const long long slot = slot_next;
+    const int pos = pos_next;
+    if (t + (int)gridDim.x < a.tokens) fetch(t + gridDim.x);
+    const long long page = slot >> a.p.page_shift;
+    bool write = slot >= 0, turn_ok = true;
+    if (write && page >= a.p.num_pages) {
+      write = false;
+      if (teller && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
+    }
+    if (a.table) {
+      if (pos < 0 || pos >= a.max_positions) {
+        if (teller && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
+        write = turn_ok = false;
+      } else if (turned) {
+        const float* row = a.table + (long long)pos * a.rot;
+        const float2 nz = make_float2(a.neg_zero, a.neg_zero);
+        uint32_t(&W)[2][8] = reinterpret_cast<uint32_t(&)[2][8]>(w);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {     // the angles of pairs i + 2 e, i + 2 e + 1
-          const float2 c2 = e ? make_float2(c.z, c.w) : make_float2(c.x, c.y);
-          const float2 s2 = e ? make_float2(s.z, s.w) : make_float2(s.x, s.y);
-          // INTER: pair i is word i of the thread's 16
-          uint32_t& wa = INTER ? W[q >> 1][4 * (q & 1) + 2 * e] : W[0][2 * q + e];
-          uint32_t& wb = INTER ? W[q >> 1][4 * (q & 1) + 2 * e + 1] : W[1][2 * q + e];
-          const float2 u = INTER ? make_float2(bf_lo(wa), bf_lo(wb)) : make_float2(bf_lo(wa), bf_hi(wa));
-          const float2 v = INTER ? make_float2(bf_hi(wa), bf_hi(wb)) : make_float2(bf_lo(wb), bf_hi(wb));
-          const float2 a2 = sub2(fma2(u, c2, nz), fma2(v, s2, nz));
-          const float2 b2 = add2(fma2(v, c2, nz), fma2(u, s2, nz));
-          wa = INTER ? pack_bf16(a2.x, b2.x) : pack_bf16(a2.x, a2.y);
-          wb = INTER ? pack_bf16(a2.y, b2.y) : pack_bf16(b2.x, b2.y);
+        for (int q = 0; q < 4; ++q) {       // four pairs of each of two words of either block (INTER: of one word)
+          const int i = INTER ? (d0 >> 1) + 4 * q : d0 + 4 * q;
+          if (INTER && 2 * i >= a.rot) continue;
+          const float4 c = __ldg(reinterpret_cast<const float4*>(row + i));
+          const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + i));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {     // the angles of pairs i + 2 e, i + 2 e + 1
+            const float2 c2 = e ? make_float2(c.z, c.w) : make_float2(c.x, c.y);
+            const float2 s2 = e ? make_float2(s.z, s.w) : make_float2(s.x, s.y);
+            // INTER: pair i is word i of the thread's 16
+            uint32_t& wa = INTER ? W[q >> 1][4 * (q & 1) + 2 * e] : W[0][2 * q + e];
+            uint32_t& wb = INTER ? W[q >> 1][4 * (q & 1) + 2 * e + 1] : W[1][2 * q + e];
+            const float2 u = INTER ? make_float2(bf_lo(wa), bf_lo(wb)) : make_float2(bf_lo(wa), bf_hi(wa));
+            const float2 v = INTER ? make_float2(bf_hi(wa), bf_hi(wb)) : make_float2(bf_lo(wb), bf_hi(wb));
+            const float2 a2 = sub2(fma2(u, c2, nz), fma2(v, s2, nz));
+            const float2 b2 = add2(fma2(v, c2, nz), fma2(u, s2, nz));
+            wa = INTER ? pack_bf16(a2.x, b2.x) : pack_bf16(a2.x, a2.y);
+            wb = INTER ? pack_bf16(a2.y, b2.y) : pack_bf16(b2.x, b2.y);
+          }
         }
       }
     }
-  }
-  if (kind == 0 && turn_ok) {
-    uint16_t* dst = a.q_out + (long long)t * a.q_out_ld + h * a.p.dim;
-    store32<WIDE>(dst + d0, w[0]);
-    store32<WIDE>(dst + d1, w[1]);
-  } else if ((kind == 1 || kind == 2) && write) {
-    const TScale ts = make_tscale(__ldg((kind == 1 ? a.p.kst : a.p.vst) + h));
-    const long long row = ((long long)h << a.p.page_shift) + (slot & ((1 << a.p.page_shift) - 1));
-    uint8_t* codes = (kind == 1 ? a.p.kc : a.p.vc) + page * a.p.codes_stride + row * (a.p.dim >> 1);
-    uint8_t* scales = (kind == 1 ? a.p.ks : a.p.vs) + page * a.p.scales_stride + row * (a.p.dim >> 4);
-    bool good = true;
+    if (kind == 0 && turn_ok) {
+      uint16_t* dst = a.q_out + (long long)t * a.q_out_ld + h * a.p.dim;
+      store32<WIDE>(dst + d0, w[0]);
+      store32<WIDE>(dst + d1, w[1]);
+    } else if ((kind == 1 || kind == 2) && write) {
+      const TScale ts = make_tscale(__ldg((kind == 1 ? a.p.kst : a.p.vst) + h));
+      const long long row = ((long long)h << a.p.page_shift) + (slot & ((1 << a.p.page_shift) - 1));
+      uint8_t* codes = (kind == 1 ? a.p.kc : a.p.vc) + page * a.p.codes_stride + row * (a.p.dim >> 1);
+      uint8_t* scales = (kind == 1 ? a.p.ks : a.p.vs) + page * a.p.scales_stride + row * (a.p.dim >> 4);
+      bool good = true;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int d = b ? d1 : d0;
-      uint32_t cw[2], sc;
-      good &= quantize_block<F46>(w[b], ts, a.neg_zero, cw, sc);
-      *reinterpret_cast<uint2*>(codes + (d >> 1)) = make_uint2(cw[0], cw[1]);
-      scales[d >> 4] = (uint8_t)sc;
+      for (int b = 0; b < 2; ++b) {
+        const int d = b ? d1 : d0;
+        uint32_t cw[2], sc;
+        good &= quantize_block<F46>(w[b], ts, a.neg_zero, cw, sc);
+        *reinterpret_cast<uint2*>(codes + (d >> 1)) = make_uint2(cw[0], cw[1]);
+        scales[d >> 4] = (uint8_t)sc;
+      }
+      if (!good && a.status) atomicOr(a.status, FOS_STATUS_NONFINITE);
     }
-    if (!good && a.status) atomicOr(a.status, FOS_STATUS_NONFINITE);
   }
 }
 
@@ -316,10 +331,15 @@ cudaError_t append(const KvAppendArgs& a, cudaStream_t st) {
     else      k_kv_append_odd<F46, false><<<grid, kThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
-  // a token's rows in CTAs of equal size, up to 256 threads
+  // a token's rows in CTAs of equal size, up to 256 threads; as many CTAs as fit
   const int all = rows * (a.p.dim / 32), ctas = (all + 255) / 256;
   const int threads = ((all + ctas - 1) / ctas + 31) / 32 * 32;
-  const dim3 grid(a.tokens, ctas);
+  static KvDevices devices;
+  int sms = 0;
+  const cudaError_t e = devices.get((const void*)k_kv_append<F46, INTER, true>, 0, &sms);
+  if (e != cudaSuccess) return e;
+  const int fit = sms * (kAppendWarps * 32 / threads), most = fit > ctas ? fit / ctas : 1;
+  const dim3 grid(a.tokens < most ? a.tokens : most, ctas);
   if (wide) k_kv_append<F46, INTER, true><<<grid, threads, 0, st>>>(a);
   else      k_kv_append<F46, INTER, false><<<grid, threads, 0, st>>>(a);
   return cudaGetLastError();
