@@ -155,16 +155,51 @@ struct Item {
   int b, rt, q0, n, len, lo, hi, base, tiles;
 };
 
+// The rows rt of a sequence whose q0, n and len are set.
+__device__ __forceinline__ void set_rows(const KvAttnArgs& a, Item& it, int rt) {
+  it.rt = rt;
+  const int first = fdiv(it.rt * kRows, a.by_group);
+  const int last = fdiv(min(it.n * a.group - 1, it.rt * kRows + kRows - 1), a.by_group);
+  it.hi = query_hi(a, it.n, it.len, last);
+  it.lo = query_lo(a, query_hi(a, it.n, it.len, first));
+  it.base = it.lo & ~15;
+  it.tiles = (it.hi - it.base + kTileTok - 1) / kTileTok;
+}
+
 // Item number `want` over all sequences (the last rows of a sequence, which
-// see the most, first); every thread of the block takes part.  False beyond
-// the last item.
-__device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int threads, Item* out, int* warp_sum,
-                                          bool tell) {
-  const int tid = threadIdx.x, per = (a.batch + threads - 1) / threads;
+// see the most, first); every thread of the block takes part and has it in
+// `it`.  False beyond the last item.  Up to 32 sequences: every warp by itself,
+// a sequence for each lane; more: the block together, through shared memory.
+__device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int threads, Item& it, Item* shared,
+                                          int* warp_sum, bool tell) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  bool bad = false, wrong;
+  if (a.batch <= 32) {
+    int nrt = 0;
+    if (lane < a.batch) {
+      lengths_of(a, lane, it.q0, it.n, it.len, wrong);
+      bad = wrong;
+      nrt = (it.n * a.group + kRows - 1) / kRows;
+    }
+    if (bad && tell && tid < 32 && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
+    int upto = nrt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const uint32_t beyond = __ballot_sync(~0u, want < upto);
+    if (!beyond) return false;
+    it.b = __ffs(beyond) - 1;
+    it.q0 = __shfl_sync(~0u, it.q0, it.b);
+    it.n = __shfl_sync(~0u, it.n, it.b);
+    it.len = __shfl_sync(~0u, it.len, it.b);
+    set_rows(a, it, __shfl_sync(~0u, upto, it.b) - 1 - want);
+    return true;
+  }
+  const int per = (a.batch + threads - 1) / threads;
   const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
   int mine = 0;
-  bool bad = false, wrong;
-  Item it;
   for (int b = b0; b < b1; ++b) {
     lengths_of(a, b, it.q0, it.n, it.len, wrong);
     bad |= wrong;
@@ -175,10 +210,10 @@ __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int thr
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(~0u, upto, o);
-    if ((tid & 31) >= o) upto += x;
+    if (lane >= o) upto += x;
   }
-  if ((tid & 31) == 31) warp_sum[tid >> 5] = upto;
-  if (tid == 0) out->b = -1;
+  if (lane == 31) warp_sum[tid >> 5] = upto;
+  if (tid == 0) shared->b = -1;
   __syncthreads();
   for (int w = 0; w < (tid >> 5); ++w) upto += warp_sum[w];
   int at = upto - mine;
@@ -188,20 +223,15 @@ __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int thr
       const int nrt = (it.n * a.group + kRows - 1) / kRows;
       if (want < at + nrt) {
         it.b = b;
-        it.rt = nrt - 1 - (want - at);
-        const int first = fdiv(it.rt * kRows, a.by_group);
-        const int last = fdiv(min(it.n * a.group - 1, it.rt * kRows + kRows - 1), a.by_group);
-        it.hi = query_hi(a, it.n, it.len, last);
-        it.lo = query_lo(a, query_hi(a, it.n, it.len, first));
-        it.base = it.lo & ~15;
-        it.tiles = (it.hi - it.base + kTileTok - 1) / kTileTok;
-        *out = it;
+        set_rows(a, it, nrt - 1 - (want - at));
+        *shared = it;
         break;
       }
       at += nrt;
     }
   __syncthreads();
-  return out->b >= 0;
+  it = *shared;
+  return it.b >= 0;
 }
 
 // One 8-value word of codes times its block's scale -> 16 bytes
@@ -255,23 +285,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
   Item* item = reinterpret_cast<Item*>(smem + C::kOffMisc + 16);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) *fail = 0;
-  if (!find_item(a, blockIdx.x / a.p.heads, kThreads, item, reinterpret_cast<int*>(smem + C::kOffMisc + 128),
-                 blockIdx.x == 0 && blockIdx.y == 0))
-    return;
-  const Item it = *item;
-  const int h = blockIdx.x % a.p.heads;
-  const int rows = it.n * a.group - it.rt * kRows;           // of this item, may exceed kRows
-  const int nt = rows > kTileRows ? 2 : 1;                   // tiles with rows
-  const int j0 = (int)((long long)it.tiles * blockIdx.y / gridDim.y);
-  const int J = (int)((long long)it.tiles * (blockIdx.y + 1) / gridDim.y) - j0;
-  const int tok_base = it.base + j0 * kTileTok;
-
   if (tid == 0) {
+    *fail = 0;
     auto init = [&](int b, int count) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar + 8 * b), "r"(count) : "memory");
     };
-    init(B_Q, 4 * nt);
+    init(B_Q, 8);
     for (int s = 0; s < 2; ++s) {
       init(B_KFULL + s, 4);
       init(B_KEMPTY + s, 1);
@@ -289,10 +308,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
                  :: "r"(smem_u32((const void*)tmem_slot)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  Item mine;
+  const bool found = find_item(a, blockIdx.x / a.p.heads, kThreads, mine, item,
+                               reinterpret_cast<int*>(smem + C::kOffMisc + 128), blockIdx.x == 0 && blockIdx.y == 0);
+  const int h = blockIdx.x % a.p.heads;
+  const int here = found ? mine.n * a.group - mine.rt * kRows : 0;
+  // The queries of a softmax warp's 32 rows, a row for D / 8 lanes at a time,
+  // are on their way before the block meets.
+  constexpr int kLanes = D / 8, kStep = 32 / kLanes;
+  const int chunk = lane & (kLanes - 1);
+  uint4 qw[kLanes];
+  if (warp < 8 && (warp >> 2) * kTileRows < here) {
+#pragma unroll
+    for (int y = 0; y < kLanes; ++y) {
+      const int rr = min(mine.rt * kRows + warp * 32 + y * kStep + lane / kLanes, mine.n * a.group - 1);
+      const int i = (int)fdiv(rr, a.by_group);
+      qw[y] = __ldg(reinterpret_cast<const uint4*>(a.q + (long long)(mine.q0 + i) * a.q_ld +
+                                                   (long long)(h * a.group + (rr - i * a.group)) * D) + chunk);
+    }
+  }
+  if (tid == 0) *item = mine;        // read again where it is used, to hold no registers
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (!found) {
+    if (warp == 12)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+    return;
+  }
+  const Item it = *item;
+  const int rows = it.n * a.group - it.rt * kRows;           // of this item, may exceed kRows
+  const int nt = rows > kTileRows ? 2 : 1;                   // tiles with rows
+  const int j0 = (int)((long long)it.tiles * blockIdx.y / gridDim.y);
+  const int J = (int)((long long)it.tiles * (blockIdx.y + 1) / gridDim.y) - j0;
+  const int tok_base = it.base + j0 * kTileTok;
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
@@ -301,24 +351,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
     const int r = it.rt * kRows + t * kTileRows + rl;
     const bool live = r < it.n * a.group;
     const int qi = live ? (int)fdiv(r, a.by_group) : 0, hq = h * a.group + (live ? r - qi * a.group : 0);
+    float vst = 0.0f;
+    if (t >= nt && lane == 0) mbar_arrive(bar + 8 * B_Q);
     if (t < nt) {
-      // the warp's 32 queries, a row for D / 8 lanes at a time, scaled by a
-      // power of two (and the sign of the softmax scale, so that larger scores
-      // are larger weights)
-      const float kst = a.scale_log2 * a.p.kst[h];
+      // the warp's 32 queries, scaled by a power of two (and the sign of the
+      // softmax scale, so that larger scores are larger weights)
+      const float kst = a.scale_log2 * __ldg(a.p.kst + h);
+      vst = __ldg(a.p.vst + h);
       uint8_t* qt = smem + C::kOffQ + t * C::kOperand;
       float* scales = reinterpret_cast<float*>(smem + C::kOffScale) + t * kTileRows + (warp & 3) * 32;
-      constexpr int kLanes = D / 8, kStep = 32 / kLanes;
-      const int chunk = lane & (kLanes - 1);
-      // all of the warp's loads are on their way before the first is used
-      uint4 qw[kLanes];
-#pragma unroll
-      for (int y = 0; y < kLanes; ++y) {
-        const int rr = min(it.rt * kRows + t * kTileRows + (warp & 3) * 32 + y * kStep + lane / kLanes,
-                           it.n * a.group - 1), i = (int)fdiv(rr, a.by_group);
-        qw[y] = __ldg(reinterpret_cast<const uint4*>(a.q + (long long)(it.q0 + i) * a.q_ld +
-                                                     (long long)(h * a.group + (rr - i * a.group)) * D) + chunk);
-      }
       uint32_t tops[kLanes];
 #pragma unroll
       for (int y = 0; y < kLanes; ++y) {
@@ -338,10 +379,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
         const uint32_t top = tops[r8], x4[4] = {qw[r8].x, qw[r8].y, qw[r8].z, qw[r8].w};
         uint32_t y[4];
         const RowScale sc = row_scale(top);
-        const float up1 = kst < 0.0f ? -sc.up1 : sc.up1;
+        float up1 = there && sc.finite ? (kst < 0.0f ? -sc.up1 : sc.up1) : 0.0f;
+        // one factor does unless the row's largest value is below 2^-113
+        const bool tiny = __any_sync(~0u, top < (14u << 23));
+        if (!tiny) up1 *= sc.up2;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          y[e] = there && sc.finite ? pack_h2(bf_lo(x4[e]) * up1 * sc.up2, bf_hi(x4[e]) * up1 * sc.up2) : 0u;
+        for (int e = 0; e < 4; ++e) {
+          float lo = bf_lo(x4[e]) * up1, hi = bf_hi(x4[e]) * up1;
+          if (tiny) { lo *= sc.up2; hi *= sc.up2; }
+          y[e] = sc.finite ? pack_h2(lo, hi) : 0u;
+        }
         *reinterpret_cast<uint4*>(qt + (chunk >> 3) * C::kHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
             make_uint4(y[0], y[1], y[2], y[3]);
         if (chunk == 0) scales[x] = sc.finite ? fabsf(kst) * sc.down1 * sc.down2 : CUDART_NAN_F;
@@ -436,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
       const bool split = gridDim.y > 1;
       const long long row = (long long)(it.q0 + qi) * a.q_heads + hq;
       const long long all = (long long)a.total_q * a.q_heads;
-      const float f = l == 0.0f ? 0.0f : __fdividef(a.p.vst[h], l);
+      const float f = l == 0.0f ? 0.0f : __fdividef(vst, l);
       const bool none = l == 0.0f || J == 0 || !ok;
       uint8_t* ot = smem + C::kOffQ + t * C::kOperand + (warp & 3) * 32 * D * 2;
 #pragma unroll 1
@@ -625,10 +672,10 @@ template <int D>
 __global__ void __launch_bounds__(256) k_kv_prompt_join(const KvAttnArgs a, const float* part, int splits) {
   __shared__ Item item;
   __shared__ int sums[8];
-  const bool found = find_item(a, blockIdx.x / a.p.heads, 256, &item, sums, false);
+  Item it;
+  const bool found = find_item(a, blockIdx.x / a.p.heads, 256, it, &item, sums, false);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!found) return;
-  const Item it = item;
   const int h = blockIdx.x % a.p.heads;
   const long long all = (long long)a.total_q * a.q_heads;
   const float2* stat = reinterpret_cast<const float2*>(part + (long long)splits * all * D);
