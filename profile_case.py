@@ -20,7 +20,7 @@ a reduced batch so a capture stays small), runs one untimed call, then
   linear    one step of the quantized Linear layer, 8192 x 4096 -> 4096: forward,
             dgrad and wgrad with x and dy quantized in the step (several kernels)
   kv_append 8192 rotated tokens appended to a cache (32 query heads, 8 key/value heads of 128)
-  kv_read   their keys and values read back
+  kv_read   the keys and values of 131072 tokens read back
   kv_decode one query for each of 4 * experts sequences over 262144 cached tokens in all
   kv_prompt the attention of a prompt of `rows` tokens
 """
@@ -113,7 +113,7 @@ def main():
             _, qx_t = F.linear_forward(xl, qw, save_colwise=True, seed=7)
             F.linear_backward(dyl, None, qw, seed=7, qx_t=qx_t)
     elif c.startswith("kv_"):
-        n = {"kv_decode": 32 * 8192, "kv_prompt": args.rows}.get(c, 8192)
+        n = {"kv_read": 16 * 8192, "kv_decode": 32 * 8192, "kv_prompt": args.rows}.get(c, 8192)
         g = torch.Generator(device=dev).manual_seed(0)
         cache = F.KVCache.empty(n // 64, 64, 8, 128, 5.0, 5.0, device=dev)
         slots = torch.randperm(n // 64, generator=g, device=dev)[:, None] * 64 + torch.arange(64, device=dev)
