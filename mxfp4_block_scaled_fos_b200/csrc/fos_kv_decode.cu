@@ -54,8 +54,8 @@ constexpr int kSlice = 16, kTile = 128;               // tokens of one copy, of 
 constexpr int kStagesK = 2, kStagesV = 3;             // tiles of a group in shared memory
 // What beginning an item costs, in tiles.  Without it a share of many short
 // items takes far longer than its tiles say: 64 ragged contexts of up to
-// 16384 tokens 209 us with 0, 155 with 3, 151 with 8, 152 with 12; 48 windows
-// of 1000 tokens 47, 35, 31, 31 us.
+// 16384 tokens 209 us with 0, 154 with 4 to 8, 156 with 10; 48 windows of 1000
+// tokens 47, 34, 32 (8) and 32 us.
 constexpr int kOver = 8;
 constexpr int kMaxCtas = 320;                         // shares: two CTAs on each of up to 160 SMs
 constexpr float kNone = -1e30f;                       // the maximum of a row that has seen nothing
