@@ -92,6 +92,7 @@ cudaError_t launch_kv_decode(const KvAttnArgs& a, int rows, float* part, cudaStr
 // many queries; splits: CTAs that share the tokens of 256 rows
 int kv_prompt_splits(long long total_q, long long batch, long long group, long long heads, long long max_q,
                      long long max_kv);
+bool kv_prompt_fits(long long total_q, long long batch, long long group, long long heads);   // in a grid
 size_t kv_prompt_workspace_bytes(int dim, int splits, long long rows);
 cudaError_t launch_kv_prompt(const KvAttnArgs& a, int splits, float* part, cudaStream_t st);
 

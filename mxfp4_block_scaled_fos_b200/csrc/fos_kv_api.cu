@@ -74,7 +74,7 @@ AttnPlan attn_plan(const fos_kv_cache* c, int64_t total_q, int64_t batch, int64_
                    int64_t max_kv) {
   AttnPlan p{};
   const int64_t group = q_heads / c->heads, rows = max_q * group, items = batch * c->heads;
-  p.many = rows > 32 && rows > 512 / (items > 0 ? items : 1);
+  p.many = rows > 32 && rows > 512 / (items > 0 ? items : 1) && kv_prompt_fits(total_q, batch, group, c->heads);
   if (p.many) {
     p.splits = kv_prompt_splits(total_q, batch, group, c->heads, max_q, max_kv);
     p.bytes = kv_prompt_workspace_bytes((int)c->head_dim, p.splits, total_q * q_heads);

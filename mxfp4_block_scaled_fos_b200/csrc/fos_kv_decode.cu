@@ -834,7 +834,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     }
     __syncthreads();
   }
-  if (dead && a.status) atomicOr(a.status, FOS_STATUS_TIMEOUT);
+  if (dead) {                    // let this warp's products finish before the tensor memory is freed
+    if (lane == 0) {
+      const uint32_t bar_d = sbase + C::kOffPlan + 128 + 8 * warp;   // the plan's sums, long read
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(bar_d) : "memory");
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                   :: "r"(bar_d) : "memory");
+      mbar_wait(bar_d, 0);
+      if (a.status) atomicOr(a.status, FOS_STATUS_TIMEOUT);
+    }
+    __syncwarp();
+  }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (warp == kWarps - 1) {

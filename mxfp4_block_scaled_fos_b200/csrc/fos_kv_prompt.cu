@@ -722,7 +722,6 @@ cudaError_t launch(const KvAttnArgs& a, int splits, float* part, cudaStream_t st
   cudaError_t e = devices.get((const void*)k_kv_prompt<D>, C::kSmem, &sms);
   if (e != cudaSuccess) return e;
   const long long grid = item_bound(a.total_q, a.batch, a.group) * a.p.heads;
-  if (grid > 0x7fffffffll) return cudaErrorNotSupported;
   k_kv_prompt<D><<<dim3((unsigned)grid, splits), kThreads, C::kSmem, st>>>(a, part);
   if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
   cudaLaunchConfig_t cfg = {};
@@ -749,7 +748,14 @@ int kv_prompt_splits(long long total_q, long long batch, long long group, long l
   const long long tiles = (max_kv + kTileTok - 1) / kTileTok;
   long long s = items >= 148 ? 1 : 148 / items;
   if (s > tiles / 4) s = tiles / 4;
+  // the workspace holds every row of q, those of no sequence too: at most four CTAs' rows for each SM
+  const long long held = ((total_q * group + kRows - 1) / kRows) * heads;
+  if (s > 4 * 148 / held) s = 4 * 148 / held;
   return s < 1 ? 1 : (int)s;
+}
+
+bool kv_prompt_fits(long long total_q, long long batch, long long group, long long heads) {
+  return item_bound(total_q, batch, group) * heads <= 0x7fffffffll;
 }
 
 size_t kv_prompt_workspace_bytes(int dim, int splits, long long rows) {

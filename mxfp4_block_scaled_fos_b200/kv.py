@@ -294,7 +294,8 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, pages: tor
         if stream is not None:
             workspace.record_stream(stream)
     elif workspace is not None:
-        _need(workspace.get_device() == cache._dev, "workspace must be on the cache's device")
+        _need(workspace.get_device() == cache._dev and workspace.is_contiguous(),
+              "workspace must be contiguous and on the cache's device")
         need = workspace.numel() * workspace.element_size()
     _call(cache, "fos_kv_attention", L.fos_kv_attention, stream,
           (cache._ref, q.data_ptr(), q_ld, t, hq, cu, b, table, most, lens, max_q,

@@ -635,7 +635,8 @@ def test_binding_refusals():
         with pytest.raises(TypeError):
             att(**kw)
     for kw in (dict(q=q[:, :3]), dict(q=q[0]), dict(pages=pages[0]), dict(lens=lens.expand(2)), dict(window=-1),
-               dict(window=5, causal=False), dict(out=q[:2]), dict(cu=cu[:0])):
+               dict(window=5, causal=False), dict(out=q[:2]), dict(cu=cu[:0]),
+               dict(workspace=torch.zeros(1, dtype=torch.uint8, device=dev).expand(1 << 24))):
         with pytest.raises(ValueError):
             att(**kw)
     for kw in (dict(n=-1), dict(scale=math.nan), dict(workspace=torch.zeros(16, dtype=torch.uint8, device=dev))):
@@ -645,3 +646,10 @@ def test_binding_refusals():
         F.kv_read(c, slots, out=(k[:2], k))
     with pytest.raises(TypeError):
         F.kv_read(c, slots.int())
+
+
+def test_a_buffer_longer_than_its_sequences_needs_no_workspace_for_the_rest():
+    """Rows of no sequence (a padded buffer) do not make the workspace grow with the CTAs of a row."""
+    cache = F.KVCache.empty(1, 64, 1, 128, 1.0, 1.0, device=require_gpu())
+    size = lambda rows: F.kv_attention_workspace_size(cache, rows, 1, 8, 300, 1 << 12)  # noqa: E731
+    assert 0 < size(300) and size(1 << 20) <= 4 * 148 * 256 * 130 * 4
