@@ -954,6 +954,10 @@ size_t kv_decode_workspace_bytes(int dim, int rows) {
   return (size_t)2 * kMaxCtas * (rows <= 8 ? 8 : 16) * (dim + 2) * 4;
 }
 
+// More than 8 rows take one tile of 16 (one CTA on an SM) rather than two of 8
+// that read the cache twice.  16 rows, 8 heads of 128, us: 32 ragged contexts of
+// up to 16384 tokens 119 against 148, 16 of 4000 45 / 52, 16 of 1000 29 / 27, 64
+// of 300 45 / 45.
 cudaError_t launch_kv_decode(const KvAttnArgs& a, int rows, float* part, cudaStream_t st) {
   if (a.p.dim == 128) return rows <= 8 ? launch<128, 1>(a, part, st) : launch<128, 2>(a, part, st);
   return rows <= 8 ? launch<64, 1>(a, part, st) : launch<64, 2>(a, part, st);

@@ -32,7 +32,9 @@
 // 6 chunks of up to 1501 queries, window 2048, head_dim 64, 107 us; 8 x 448
 // queries over up to 1500 tokens, 16 heads of 64, 32 us.  Slower: two threads
 // a row (875 us), a polynomial for a quarter of the exponentials (642 against
-// 631 without), the weights handed over in halves (625 against 629: no gain).
+// 631 without), the weights handed over in halves (625 against 629: no gain), 64
+// tokens a turn with two score buffers a tile (602 against 541: an MMA of 64
+// tokens takes as long as one of 128).
 #include <math_constants.h>
 
 #include "fos_kv.cuh"
@@ -94,34 +96,36 @@ __device__ __forceinline__ uint32_t desc_mn(uint32_t addr, uint32_t half) {
   return ((addr & 0x3FFFF) >> 4) | ((half >> 4) << 16);
 }
 
-// The MMAs and commits run converged, predicated on one lane, so that their
-// operands stay in uniform registers: issued from a branch of one thread an
-// MMA took 75 cycles, more than the 64 that the tensor core needs for it.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
-                                       uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
-      :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(lead), "r"(kDescHi) : "memory");
+// One lane of the (converged) warp, the same each time: commits cover the
+// MMAs of the thread that issues them.  A branch on elect.sync keeps the
+// operands in uniform registers: 8192 causal queries 530 us, 541 with each MMA
+// predicated on lane 0, 5 % more again from a branch on lane 0.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
-                                       uint32_t lead) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "mov.b64 db, {%2, %6};\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
-      :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(lead), "r"(kDescHi) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi) : "memory");
 }
 
-__device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-      :: "r"(bar), "r"(lead) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi) : "memory");
+}
+
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
 }
 
 #define FOS_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
@@ -603,7 +607,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
     // ---------------------------------------------------------------- MMAs
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 12 && J > 0) {
-      const uint32_t lead = lane == 0;
       const uint32_t dq = desc_k(sbase + C::kOffQ), dk = desc_k(sbase + C::kOffK);
       const uint32_t dv = desc_mn(sbase + C::kOffV, C::kHalf);
       constexpr uint32_t kStep = C::kOperand >> 4;    // from one tile or stage to the next
@@ -611,40 +614,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint32_t at = ((i >> 2) * C::kHalf + (i & 3) * 32) >> 4;
-          mma_ss(tmem + C::kColS + 128 * t, dq + t * kStep + at, dk + stage * kStep + at, C::kIdescS, i > 0, lead);
+          mma_ss(tmem + C::kColS + 128 * t, dq + t * kStep + at, dk + stage * kStep + at, C::kIdescS, i > 0);
         }
-        commit(bar + 8 * (B_S + t), lead);
+        commit(bar + 8 * (B_S + t));
       };
-      bool ok = mbar_wait(bar + 8 * B_Q, 0, fail) && mbar_wait(bar + 8 * B_KFULL, 0, fail);
+      // the warp stays together, a wait that gave up included
+      auto wait = [&](int b, uint32_t parity) { return __all_sync(~0u, mbar_wait(bar + 8 * b, parity, fail)) != 0; };
+      bool ok = wait(B_Q, 0) && wait(B_KFULL, 0);
       if (ok) {
         fence_after();
-        for (int t = 0; t < nt; ++t) scores(t, 0);
-        commit(bar + 8 * B_KEMPTY, lead);
+        if (elect()) {
+          for (int t = 0; t < nt; ++t) scores(t, 0);
+          commit(bar + 8 * B_KEMPTY);
+        }
+        __syncwarp();
       }
 #pragma unroll 1
       for (int j = 0; ok && j < J; ++j) {
         const uint32_t s = j & 1, s1 = s ^ 1;
         // keys and values are there long before the weights as a rule
-        ok = mbar_wait(bar + 8 * (B_VFULL + s), (j >> 1) & 1, fail) &&
-             (j + 1 >= J || mbar_wait(bar + 8 * (B_KFULL + s1), ((j + 1) >> 1) & 1, fail));
+        ok = wait(B_VFULL + s, (j >> 1) & 1) && (j + 1 >= J || wait(B_KFULL + s1, ((j + 1) >> 1) & 1));
 #pragma unroll 1
         for (int t = 0; ok && t < nt; ++t) {
-          ok = mbar_wait(bar + 8 * (B_P + t), j & 1, fail);
+          ok = wait(B_P + t, j & 1);
           if (!ok) break;
           fence_after();
+          if (elect()) {
 #pragma unroll
-          for (int i = 0; i < kTileTok / 16; ++i)
-            mma_ts(tmem + C::kColO + 128 * t, tmem + C::kColS + 128 * t + 8 * i, dv + s * kStep + (i * 2048 >> 4),
-                   C::kIdescO, j > 0 || i > 0, lead);
-          if (j + 1 < J) scores(t, s1);
-          else           commit(bar + 8 * (B_O + t), lead);
+            for (int i = 0; i < kTileTok / 16; ++i)
+              mma_ts(tmem + C::kColO + 128 * t, tmem + C::kColS + 128 * t + 8 * i, dv + s * kStep + (i * 2048 >> 4),
+                     C::kIdescO, j > 0 || i > 0);
+            if (j + 1 < J) scores(t, s1);
+            else           commit(bar + 8 * (B_O + t));
+          }
+          __syncwarp();
         }
         // of tile j, all products; of tile j + 1, the scores
-        commit(bar + 8 * (B_VEMPTY + s), lead);
-        if (j + 1 < J) commit(bar + 8 * (B_KEMPTY + s1), lead);
+        if (elect()) {
+          commit(bar + 8 * (B_VEMPTY + s));
+          if (j + 1 < J) commit(bar + 8 * (B_KEMPTY + s1));
+        }
+        __syncwarp();
       }
       if (!ok) {   // let what was issued finish before the tensor memory is freed
-        commit(bar + 8 * B_DRAIN, lead);
+        if (elect()) commit(bar + 8 * B_DRAIN);
+        __syncwarp();
         for (uint32_t i = 0; i < kWaitLimit; ++i) {
           uint32_t done;
           asm volatile(
