@@ -37,8 +37,8 @@
 // score passes it by 2^8 (fos_kv.cuh).
 //
 // Measured: 64 sequences of up to 16384 tokens (598 MB of 8 heads of 128,
-// pages of 16) 149 us with k_kv_join, 0.62 of the copy bandwidth; 4 of up to
-// 131072 tokens (407 MB) 102 us, 0.62; one of 1000 tokens 11 us.  A CTA in the
+// pages of 16) 148 us with k_kv_join, 0.63 of the copy bandwidth; 4 of up to
+// 131072 tokens (407 MB) 101 us, 0.62; one of 1000 tokens 11 us.  A CTA in the
 // middle of a long item reads at 0.95 of it; beginning an item costs it 5 to
 // 7 us (page ids, digits, the first scores, the warps' results joined), which
 // the other CTA of the SM covers in part, and the plan 2 us.
