@@ -484,15 +484,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
       }
       if (J > 0 && ok) ok = __all_sync(~0u, mbar_wait(bar + 8 * (B_O + t), 0, fail));
       fence_after();
-      // the output: a warp's rows through shared memory (its queries', which
-      // no product reads any more), so that whole rows are written at once
+      // the output: a warp's rows through shared memory, each where the query of
+      // its row was, so that whole rows are written at once.  No product reads the
+      // queries any more, and a warp touches no bytes but its own queries': the
+      // other warps may still be writing theirs when there are no tokens to wait for.
       const float msc = m == -CUDART_INF_F ? -CUDART_INF_F : m * rs;
       const bool split = gridDim.y > 1;
       const long long row = (long long)(it.q0 + qi) * a.q_heads + hq;
       const long long all = (long long)a.total_q * a.q_heads;
       const float f = l == 0.0f ? 0.0f : __fdividef(vst, l);
       const bool none = l == 0.0f || J == 0 || !ok;
-      uint8_t* ot = smem + C::kOffQ + t * C::kOperand + (warp & 3) * 32 * D * 2;
+      uint8_t* ot = smem + C::kOffQ + t * C::kOperand + (warp & 3) * 32 * 128;
 #pragma unroll 1
       for (int k = 0; k < D; k += 32) {
         uint32_t o[32];
@@ -519,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
               w[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
             const int c = k / 8 + e;
-            *reinterpret_cast<uint4*>(ot + lane * D * 2 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(ot + (c >> 3) * C::kHalf + lane * 128 + (((c & 7) ^ (lane & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
         __syncwarp();
@@ -532,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
             const int i = (int)fdiv(rr, a.by_group);
             reinterpret_cast<uint4*>(a.out + (long long)(it.q0 + i) * a.out_ld +
                                      (long long)(h * a.group + (rr - i * a.group)) * D)[chunk] =
-                *reinterpret_cast<const uint4*>(ot + x * D * 2 + ((chunk ^ (x & 7)) << 4));
+                *reinterpret_cast<const uint4*>(ot + (chunk >> 3) * C::kHalf + x * 128 +
+                                                (((chunk & 7) ^ (x & 7)) << 4));
           }
         }
       }

@@ -653,3 +653,32 @@ def test_a_buffer_longer_than_its_sequences_needs_no_workspace_for_the_rest():
     cache = F.KVCache.empty(1, 64, 1, 128, 1.0, 1.0, device=require_gpu())
     size = lambda rows: F.kv_attention_workspace_size(cache, rows, 1, 8, 300, 1 << 12)  # noqa: E731
     assert 0 < size(300) and size(1 << 20) <= 4 * 148 * 256 * 130 * 4
+
+
+# the kernel for many queries, one CTA for all tokens of its rows (no workspace): whole row tiles that see no key,
+# of an empty sequence or of more queries than keys, beside others
+@pytest.mark.parametrize("dim,page,heads,group,q_len,kv_len,causal", [
+    (128, 64, 2, 2, [150, 400, 3, 260], [300, 0, 0, 500], False),
+    (128, 16, 2, 1, [600, 150], [40, 860], True),
+    (128, 128, 8, 4, [200, 129], [0, 0], False),
+    (64, 32, 2, 2, [150, 400, 3, 260], [300, 0, 0, 500], False),
+    (64, 16, 2, 1, [600, 150], [40, 860], True),
+])
+def test_rows_without_keys_in_every_run(dim, page, heads, group, q_len, kv_len, causal):
+    dev = require_gpu()
+    pages, n = _paged(kv_len, page, 120)
+    cache, ref = _random_cache(n, page, heads, dim, 121)
+    cu = [0] + np.cumsum(q_len).tolist()
+    q = _queries(cu[-1], heads * group, dim, 122, 2.0)
+    assert F.kv_attention_workspace_size(cache, cu[-1], len(q_len), heads * group, max(q_len), pages.shape[1]) == 0
+    first, _ = _check(cache, ref, q, cu, pages, kv_len, causal=causal)
+    none = torch.cat([torch.arange(m) < max(0, m - k) if causal else torch.full((m,), k == 0)
+                      for m, k in zip(q_len, kv_len)]).to(dev)
+    assert int(none.sum()) >= 256 // group
+    args = (cache, q.to(dev), torch.tensor(cu, dtype=I32, device=dev), torch.from_numpy(pages).to(dev),
+            torch.tensor(kv_len, dtype=I32, device=dev), max(q_len))
+    first = torch.from_numpy(first).to(dev, torch.bfloat16)
+    for _ in range(300):
+        out, lse = torch.full_like(first, 3.0), torch.full((cu[-1], heads * group), 3.0, device=dev)
+        F.kv_attention(*args, causal=causal, out=out, lse=lse)
+        assert torch.equal(out, first) and not out[none].any() and bool((lse[none] == -math.inf).all())
