@@ -10,7 +10,9 @@ quantizes the keys and values into their slots; kv_attention reads the codes
 and scales; kv_read gives them back as bf16.  This module only checks
 arguments, allocates outputs and workspaces, and hands pointers to the C ABI
 (include/fos.h, where layouts and semantics are).  The calls run on the
-device of their tensors, on `stream` or that device's current stream.
+device of their tensors, on `stream` or that device's current stream.  With
+`stream`, the tensors passed in must be ready on it; outputs and workspaces
+that the call allocates are that stream's.
 
 Sources: Ultralytics glossary "FP4", "Como funciona FP4" (NVFP4: 16 values,
 E4M3 block scale, FP32 scale); Hugging Face transformers doc "Four Over
@@ -139,8 +141,18 @@ def _call(cache: "KVCache", what: str, fn, stream, args) -> None:
         raise fos.FosError(st, what)
 
 
-def _empty_like(x: torch.Tensor) -> torch.Tensor:
-    return torch.empty_like(x, memory_format=torch.contiguous_format)
+def _empty(x: torch.Tensor, shape, dtype, stream, output: bool = True) -> torch.Tensor:
+    """A buffer of a call on `stream`.  It comes from that stream's own memory:
+    a block of the current stream's may still be in use by work that `stream`
+    does not wait for.  An output is also kept from reuse until the current
+    stream's work on it at its end is done."""
+    if stream is None:
+        return x.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        y = x.new_empty(shape, dtype=dtype)
+    if output:
+        y.record_stream(torch.cuda.current_stream(x.device))
+    return y
 
 
 def _rows(name: str, x: torch.Tensor, tokens: int, heads: int, cache: "KVCache") -> int:
@@ -207,7 +219,7 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
         hq = q.shape[1]
         q_ld = _rows("q", q, t, hq, cache)
         if q_out is None:
-            q_out, out_ld = _empty_like(q), hq * cache.head_dim
+            q_out, out_ld = _empty(q, q.shape, torch.bfloat16, stream), hq * cache.head_dim
         else:
             out_ld = _rows("q_out", q_out, t, hq, cache)
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
@@ -227,7 +239,7 @@ def kv_read(cache: KVCache, slots: torch.Tensor, out: Optional[Tuple[torch.Tenso
     t = slots.shape[0]
     at = _ints("slots", slots, torch.int64, (t,), cache)
     if out is None:
-        out = slots.new_empty((2, t, cache.heads, cache.head_dim), dtype=torch.bfloat16).unbind(0)
+        out = _empty(slots, (2, t, cache.heads, cache.head_dim), torch.bfloat16, stream).unbind(0)
     else:
         for x in out:
             _rows("out", x, t, cache.heads, cache)
@@ -278,21 +290,19 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, pages: tor
     cu, table = _ints("cu_q", cu_q, torch.int32, (b + 1,), cache), _ints("pages", pages, torch.int32, (b, most), cache)
     lens = _ints("kv_len", kv_len, torch.int32, (b,), cache)
     if out is None:
-        out, out_ld = _empty_like(q), hq * cache.head_dim
+        out, out_ld = _empty(q, q.shape, torch.bfloat16, stream), hq * cache.head_dim
     else:
         out_ld = _rows("out", out, t, hq, cache)
     lse_ptr = None
     if lse is not None:
         lse_ptr = _ints("lse", lse, torch.float32, (t, hq), cache)
     elif return_lse:
-        lse = q.new_empty((t, hq), dtype=torch.float32)
+        lse = _empty(q, (t, hq), torch.float32, stream)
         lse_ptr = lse.data_ptr()
     L = _lib()
     need = _workspace_bytes(cache.heads, cache.head_dim, cache.page_size, t, b, hq, max_q, most)
     if workspace is None and need:
-        workspace = q.new_empty((need,), dtype=torch.uint8)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _empty(q, (need,), torch.uint8, stream, output=False)
     elif workspace is not None:
         _need(workspace.get_device() == cache._dev and workspace.is_contiguous(),
               "workspace must be contiguous and on the cache's device")

@@ -682,3 +682,42 @@ def test_rows_without_keys_in_every_run(dim, page, heads, group, q_len, kv_len, 
         out, lse = torch.full_like(first, 3.0), torch.full((cu[-1], heads * group), 3.0, device=dev)
         F.kv_attention(*args, causal=causal, out=out, lse=lse)
         assert torch.equal(out, first) and not out[none].any() and bool((lse[none] == -math.inf).all())
+
+
+@pytest.mark.parametrize("max_q", [1, 100])
+def test_calls_that_overlap_share_no_buffers(max_q):
+    """A call on another stream while one on the current stream still runs,
+    with no wait between the streams: workspaces and outputs that the calls
+    allocate are not the other's."""
+    dev = require_gpu()
+    kv_len = [4000, 3000]
+    pages, n = _paged(kv_len, 64, 130)
+    cache, _ = _random_cache(n, 64, 2, 128, 131)
+    pd, ld = torch.from_numpy(pages).to(dev), torch.tensor(kv_len, dtype=I32, device=dev)
+    cu = torch.tensor([0, max_q, 2 * max_q], dtype=I32, device=dev)
+    qs = [_queries(2 * max_q, 8, 128, 132 + i).to(dev) for i in range(2)]
+    assert F.kv_attention_workspace_size(cache, 2 * max_q, 2, 8, max_q, pages.shape[1]) > 0
+    call = lambda q, **kw: F.kv_attention(cache, q, cu, pd, ld, max_q, return_lse=True, **kw)  # noqa: E731
+    slots = pd[0].long().clamp(min=0) * 64
+    want = [call(q) for q in qs] + [F.kv_read(cache, slots)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [call(qs[0]) if i % 2 == 0 else call(qs[1], stream=side) for i in range(6)]
+        got.append(F.kv_read(cache, slots, stream=side))
+        torch.cuda.synchronize()
+        for i, pair in enumerate(got):
+            for a, b in zip(pair, want[2 if i == 6 else i % 2]):
+                assert torch.equal(a, b), i
+    # outputs that are dropped while the current stream still reads them
+    total = torch.zeros((), dtype=torch.float64, device=dev)
+    for _ in range(50):
+        y, _ = call(qs[1], stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        total += y.double().sum()
+        del y
+    torch.cuda.synchronize()
+    one = torch.zeros((), dtype=torch.float64, device=dev)
+    for _ in range(50):
+        one += want[1][0].double().sum()
+    assert torch.equal(total, one)

@@ -111,3 +111,52 @@ def test_binding_refuses_what_is_no_cache():
         F.KVCache(t(2, 1, 16, 32, dtype=torch.uint8), None, None, None, None, None, fmt="mxfp4")
     with pytest.raises(ValueError):
         F.KVCache(t(2, 16, 32, dtype=torch.uint8), None, None, None, None, None)
+
+
+def test_buffers_of_a_call_on_another_stream_are_that_streams(L, monkeypatch):
+    """What a call with stream= allocates (outputs and workspace) comes from that
+    stream's memory, and the current stream's use of the outputs is recorded."""
+    inside, theirs, mine, recorded, calls = [], [], [], [], []
+
+    class On:
+        def __init__(self, stream):
+            assert stream == "side"
+
+        def __enter__(self):
+            inside.append(1)
+
+        def __exit__(self, *_):
+            inside.pop()
+
+    def watch(make):
+        def f(*a, **kw):
+            t = make(*a, **kw)
+            (theirs if inside else mine).append(t)
+            return t
+        return f
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
+    monkeypatch.setattr(torch.Tensor, "new_empty", watch(torch.Tensor.new_empty))
+    monkeypatch.setattr(torch, "empty_like", watch(torch.empty_like))
+    monkeypatch.setattr(torch, "empty", watch(torch.empty))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s)))
+    monkeypatch.setattr(kv, "_call", lambda cache, what, fn, stream, args: calls.append((what, stream, args)))
+
+    class Cache:
+        heads, head_dim, page_size, _dev, _fmt, _ref, _scale = 1, 64, 16, -1, 0, None, 0.125
+
+    c, i32 = Cache(), torch.int32
+    x, slots = torch.zeros(3, 1, 64, dtype=torch.bfloat16), torch.arange(3)
+    pos, table = torch.zeros(3, dtype=i32), torch.zeros(4, 64)
+    got = [kv.kv_append(c, x, x, slots, pos, table, q=x, stream="side")]
+    got += kv.kv_read(c, slots, stream="side")
+    got += kv.kv_attention(c, x, torch.tensor([0, 3], dtype=i32), torch.zeros(1, 40, dtype=i32),
+                           torch.zeros(1, dtype=i32), 3, return_lse=True, stream="side")
+    assert [w for w, *_ in calls] == ["fos_kv_append", "fos_kv_read", "fos_kv_attention"]
+    assert all(s == "side" for _, s, _ in calls) and not mine
+    ptrs = {t.data_ptr() for t in theirs}
+    workspace = calls[2][2][17]
+    assert workspace in ptrs and all(any(t.data_ptr() <= g.data_ptr() < t.data_ptr() + t.nbytes for t in theirs)
+                                     for g in got)
+    assert set(recorded) == {(p, "current") for p in ptrs - {workspace}}
