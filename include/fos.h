@@ -410,7 +410,8 @@ fos_status fos_kv_read(const fos_kv_cache* cache, const int64_t* slots, int64_t 
  *           cu_q[b + 1] - 1.  Queries outside [cu_q[0], cu_q[batch]) are not
  *           touched: their rows of out and lse stay as they were.
  *   pages   int32 [batch][max_pages]: the pages of each sequence in order;
- *           entries that hold no visible token are not read.
+ *           entries that hold no visible token are not read.  max_pages *
+ *           page_size: at most 2^31 - 65536 (FOS_ERR_SHAPE).
  *   kv_len  int32 [batch]: tokens of each sequence in the cache, those of its
  *           queries among them when causal.
  *   max_q   the largest number of queries of a sequence (it chooses between

@@ -160,3 +160,14 @@ def test_buffers_of_a_call_on_another_stream_are_that_streams(L, monkeypatch):
     assert workspace in ptrs and all(any(t.data_ptr() <= g.data_ptr() < t.data_ptr() + t.nbytes for t in theirs)
                                      for g in got)
     assert set(recorded) == {(p, "current") for p in ptrs - {workspace}}
+
+
+@pytest.mark.parametrize("page_size", [16, 32, 64, 128])
+def test_tables_whose_tokens_pass_32_bits_are_refused(L, page_size):
+    """Up to the largest length that counts past the last token's tile still fit in 32 bits for."""
+    c = _cache(page_size=page_size, codes_page_stride=1 << 14, scales_page_stride=1 << 11)
+    most = ((1 << 31) - 65536) // page_size
+    assert _attention(L, c, max_pages=most, batch=0) == 0
+    for pages in (most + 1, (1 << 31) // page_size - 1, (1 << 31) // page_size):
+        assert _attention(L, c, max_pages=pages) == SHAPE
+        assert _attention(L, c, max_pages=pages, max_q=300, total=300) == SHAPE
