@@ -181,7 +181,7 @@ fos_status fos_kv_attention(const fos_kv_cache* cache, const void* q, int64_t q_
   if (q_heads < 1 || q_heads > 65536 || q_heads % a.p.heads) return FOS_ERR_SHAPE;
   // rows and tokens are 32-bit in the kernels, which count up to the end of a tile of rows, and some 8500
   // tokens past the last one of a sequence (page ids are asked for up to 32 tiles of a group ahead)
-  if (total_q * (q_heads / a.p.heads) >= (1ll << 31) - 512 || max_pages * cache->page_size > (1ll << 31) - 65536)
+  if (total_q * (q_heads / a.p.heads) >= (1ll << 31) - 512 || max_pages > ((1ll << 31) - 65536) / cache->page_size)
     return FOS_ERR_SHAPE;
   if (batch == 0 || total_q == 0) return FOS_OK;  // buffers of nothing may be NULL
   if (!q || !cu_q || (!pages && max_pages) || !kv_len || !out) return FOS_ERR_NULL;

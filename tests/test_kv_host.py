@@ -171,3 +171,8 @@ def test_tables_whose_tokens_pass_32_bits_are_refused(L, page_size):
     for pages in (most + 1, (1 << 31) // page_size - 1, (1 << 31) // page_size):
         assert _attention(L, c, max_pages=pages) == SHAPE
         assert _attention(L, c, max_pages=pages, max_q=300, total=300) == SHAPE
+
+
+def test_a_table_width_whose_product_wraps_is_refused(L):
+    for pages in (1 << 60, (1 << 60) + 1, (1 << 63) - 1):
+        assert _attention(L, max_pages=pages) == SHAPE
