@@ -61,15 +61,20 @@ __device__ __forceinline__ int query_lo(const KvAttnArgs& a, int hi) {
   return a.window && hi > a.window ? (int)(hi - a.window) : 0;
 }
 
-// Queries and keys of sequence b, clamped to what the arguments allow.
-__device__ __forceinline__ void lengths_of(const KvAttnArgs& a, int b, int& q0, int& n, int& len, bool& bad) {
+// Queries and keys of sequence b, clamped to what the arguments allow (`bad`
+// if they had to be).  False if its offsets descend or leave the queries: then
+// no sequence is answered, for whatever counts rows and items over all of them
+// (in 32 bits, for grids and loops) relies on their adding up to total_q at most.
+__device__ __forceinline__ bool lengths_of(const KvAttnArgs& a, int b, int& q0, int& n, int& len, bool& bad) {
   const int x = a.cu_q[b], y = a.cu_q[b + 1];
   const long long cap = a.max_pages << a.p.page_shift;
   const int m = a.kv_len[b];
-  bad = x < 0 || y < x || y > a.total_q || m < 0 || m > cap;
+  const bool ordered = x >= 0 && y >= x && y <= a.total_q;
+  bad = !ordered || m < 0 || m > cap;
   q0 = x;
-  n = (x < 0 || y < x || y > a.total_q) ? 0 : y - x;
+  n = ordered ? y - x : 0;
   len = max(0, (int)min((long long)m, cap));
+  return ordered;
 }
 
 // The scaling of a query row to below 2^15 by a power of two, for its f16

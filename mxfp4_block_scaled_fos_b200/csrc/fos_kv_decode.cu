@@ -250,12 +250,11 @@ struct Item {
 };
 
 template <int ROWS>
-__device__ __forceinline__ int load_sequence(const KvAttnArgs& a, int b, Item& it) {
-  bool wrong;
-  lengths_of(a, b, it.q0, it.n, it.len, wrong);
+__device__ __forceinline__ bool load_sequence(const KvAttnArgs& a, int b, Item& it, bool& wrong) {
+  const bool ordered = lengths_of(a, b, it.q0, it.n, it.len, wrong);
   it.b = b;
   it.nrt = (it.n * a.group + ROWS - 1) / ROWS;
-  return wrong;
+  return ordered;
 }
 
 // The item after `it`; false behind the last.
@@ -266,9 +265,10 @@ __device__ __forceinline__ bool next_item(const KvAttnArgs& a, Item& it) {
   it.h = 0;
   if (++it.rt == it.nrt) {
     it.rt = 0;
+    bool wrong;
     do {
       if (++it.b >= a.batch) return false;
-      load_sequence<ROWS>(a, it.b, it);
+      load_sequence<ROWS>(a, it.b, it, wrong);
     } while (it.nrt == 0);
   }
   it.s = span_of<ROWS>(a, it.n, it.len, it.rt);
@@ -282,17 +282,18 @@ struct Plan {
 };
 
 // Every thread of the block takes part.  The item is set unless the share is
-// empty.
+// empty; with broken offsets all shares are.
 template <int ROWS>
 __device__ __forceinline__ void make_plan(const KvAttnArgs& a, int share, int shares, Plan* plan, long long* warp_sum,
                                           bool tell) {
   const int tid = threadIdx.x, per = (a.batch + kThreads - 1) / kThreads;
   const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
   long long mine = 0;
-  bool bad = false;
+  bool bad = false, ordered = true, wrong;
   Item it;
-  for (int b = b0; b < b1; ++b) {
-    bad |= load_sequence<ROWS>(a, b, it);
+  for (int b = b0; b < b1 && ordered; ++b) {
+    ordered = load_sequence<ROWS>(a, b, it, wrong);
+    bad |= wrong;
     long long tiles = 0;
     for (int rt = 0; rt < it.nrt; ++rt) tiles += span_of<ROWS>(a, it.n, it.len, rt).tiles + kOver;
     mine += tiles * a.p.heads;
@@ -305,19 +306,20 @@ __device__ __forceinline__ void make_plan(const KvAttnArgs& a, int share, int sh
     if ((tid & 31) >= o) upto += x;
   }
   if ((tid & 31) == 31) warp_sum[tid >> 5] = upto;
-  __syncthreads();
+  const bool broken = __syncthreads_or(!ordered);
   long long before = 0, total = 0;
   for (int w = 0; w < kWarps; ++w) {
     if (w < (tid >> 5)) before += warp_sum[w];
     total += warp_sum[w];
   }
   upto += before;
+  if (broken) total = upto = mine = 0;
   const long long first = Split(total, shares).first(share);
   if (tid == 0) { plan->total = total; plan->first = first; }
   if (first >= upto - mine && first < upto) {
     long long x = upto - mine;
     for (int b = b0; b < b1; ++b) {
-      if (per > 1) load_sequence<ROWS>(a, b, it);
+      if (per > 1) load_sequence<ROWS>(a, b, it, wrong);
       for (int rt = 0; rt < it.nrt; ++rt) {
         it.s = span_of<ROWS>(a, it.n, it.len, rt);
         const int each = it.s.tiles + kOver;

@@ -173,21 +173,22 @@ __device__ __forceinline__ void set_rows(const KvAttnArgs& a, Item& it, int rt) 
 
 // Item number `want` over all sequences (the last rows of a sequence, which
 // see the most, first); every thread of the block takes part and has it in
-// `it`.  False beyond the last item.  Up to 32 sequences: every warp by itself,
+// `it`.  False beyond the last item, and for all with broken offsets.  Up to 32 sequences: every warp by itself,
 // a sequence for each lane, which saves the block two meetings of a start of
 // 13000 cycles (2000 for the item, 1100 to meet); more: the block together,
 // through shared memory, a sequence for each thread at once instead of 32 in turn.
 __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int threads, Item& it, Item* shared,
                                           int* warp_sum, bool tell) {
   const int tid = threadIdx.x, lane = tid & 31;
-  bool bad = false, wrong;
+  bool bad = false, ordered = true, wrong;
   if (a.batch <= 32) {
     int nrt = 0;
     if (lane < a.batch) {
-      lengths_of(a, lane, it.q0, it.n, it.len, wrong);
+      ordered = lengths_of(a, lane, it.q0, it.n, it.len, wrong);
       bad = wrong;
       nrt = (it.n * a.group + kRows - 1) / kRows;
     }
+    if (!__all_sync(~0u, ordered)) nrt = 0;
     if (bad && tell && tid < 32 && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
     int upto = nrt;
 #pragma unroll
@@ -207,8 +208,8 @@ __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int thr
   const int per = (a.batch + threads - 1) / threads;
   const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
   int mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    lengths_of(a, b, it.q0, it.n, it.len, wrong);
+  for (int b = b0; b < b1 && ordered; ++b) {
+    ordered = lengths_of(a, b, it.q0, it.n, it.len, wrong);
     bad |= wrong;
     mine += (it.n * a.group + kRows - 1) / kRows;
   }
@@ -221,10 +222,10 @@ __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int thr
   }
   if (lane == 31) warp_sum[tid >> 5] = upto;
   if (tid == 0) shared->b = -1;
-  __syncthreads();
+  const bool broken = __syncthreads_or(!ordered);
   for (int w = 0; w < (tid >> 5); ++w) upto += warp_sum[w];
   int at = upto - mine;
-  if (want >= at && want < upto)
+  if (want >= at && want < upto && !broken)
     for (int b = b0; b < b1; ++b) {
       if (per > 1) lengths_of(a, b, it.q0, it.n, it.len, wrong);
       const int nrt = (it.n * a.group + kRows - 1) / kRows;

@@ -721,3 +721,48 @@ def test_calls_that_overlap_share_no_buffers(max_q):
     for _ in range(50):
         one += want[1][0].double().sum()
     assert torch.equal(total, one)
+
+
+@pytest.mark.parametrize("max_q", [1, 1 << 20])
+@pytest.mark.parametrize("batch,at,to", [(3, 1, 7), (3, 3, 3), (32, 31, 7), (33, 17, 0), (700, 512, 3), (700, 0, -1)])
+def test_broken_offsets_answer_no_query(batch, at, to, max_q):
+    """Offsets that descend or leave the queries anywhere: a status, and outputs as they were."""
+    dev = require_gpu()
+    cache, _ = _random_cache(3, 16, 2, 64, 140)
+    cu = list(range(0, 2 * batch + 2, 2))
+    total = cu[-1]
+    q = _queries(total, 4, 64, 141).to(dev)
+    pages = torch.zeros(batch, 2, dtype=I32, device=dev)
+    lens = torch.full((batch,), 20, dtype=I32, device=dev)
+
+    def run(cu):
+        status = torch.zeros(1, dtype=I32, device=dev)
+        out = torch.full((total, 4, 64), 3.0, dtype=torch.bfloat16, device=dev)
+        lse = torch.full((total, 4), 3.0, device=dev)
+        F.kv_attention(cache, q, torch.tensor(cu, dtype=I32, device=dev), pages, lens, max_q, out=out, lse=lse,
+                       status=status)
+        return bool((out == 3.0).any()), bool((out == 3.0).all() and (lse == 3.0).all()), int(status)
+
+    some, _, status = run(cu)
+    assert not some and status == 0
+    for value in (to, total + 1):
+        broken = list(cu)
+        broken[at] = value
+        _, untouched, status = run(broken)
+        assert untouched and status == F.STATUS_INDEX
+
+
+@pytest.mark.parametrize("max_q", [1, 1 << 14])
+def test_overlapping_sequences_whose_rows_pass_32_bits(max_q):
+    """65537 sequences, every other one with all 2^24 rows: 2^39 rows, counted
+    in 32 bits for a grid that has room for 2^24."""
+    dev = require_gpu()
+    batch, total, heads = 65537, 1 << 14, 1 << 10
+    cache, _ = _random_cache(1, 16, 1, 64, 150)
+    cu = torch.zeros(batch + 1, dtype=I32, device=dev)
+    cu[1::2] = total
+    q = torch.ones(total, heads, 64, dtype=torch.bfloat16, device=dev)
+    out, status = torch.full_like(q, 3.0), torch.zeros(1, dtype=I32, device=dev)
+    F.kv_attention(cache, q, cu, torch.zeros(batch, 1, dtype=I32, device=dev), torch.ones(batch, dtype=I32, device=dev),
+                   max_q, out=out, status=status)
+    assert int(status) == F.STATUS_INDEX and bool((out == 3.0).all())
