@@ -142,7 +142,7 @@ def _call(cache: "KVCache", what: str, fn, stream, args) -> None:
 
 
 def _empty(x: torch.Tensor, shape, dtype, stream, output: bool = True) -> torch.Tensor:
-    """A buffer of a call on `stream`.  It comes from that stream's own memory:
+    """A buffer of a call on `stream`, on x's device.  It comes from that stream's own memory:
     a block of the current stream's may still be in use by work that `stream`
     does not wait for.  An output is also kept from reuse until the current
     stream's work on it at its end is done."""
@@ -153,6 +153,12 @@ def _empty(x: torch.Tensor, shape, dtype, stream, output: bool = True) -> torch.
     if output:
         y.record_stream(torch.cuda.current_stream(x.device))
     return y
+
+
+def _empty_like(x: torch.Tensor, stream) -> torch.Tensor:
+    if stream is None:                     # 1 us less than new_empty of x.shape
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    return _empty(x, x.shape, x.dtype, stream)
 
 
 def _rows(name: str, x: torch.Tensor, tokens: int, heads: int, cache: "KVCache") -> int:
@@ -219,7 +225,7 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
         hq = q.shape[1]
         q_ld = _rows("q", q, t, hq, cache)
         if q_out is None:
-            q_out, out_ld = _empty(q, q.shape, torch.bfloat16, stream), hq * cache.head_dim
+            q_out, out_ld = _empty_like(q, stream), hq * cache.head_dim
         else:
             out_ld = _rows("q_out", q_out, t, hq, cache)
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
@@ -290,7 +296,7 @@ def kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, pages: tor
     cu, table = _ints("cu_q", cu_q, torch.int32, (b + 1,), cache), _ints("pages", pages, torch.int32, (b, most), cache)
     lens = _ints("kv_len", kv_len, torch.int32, (b,), cache)
     if out is None:
-        out, out_ld = _empty(q, q.shape, torch.bfloat16, stream), hq * cache.head_dim
+        out, out_ld = _empty_like(q, stream), hq * cache.head_dim
     else:
         out_ld = _rows("out", out, t, hq, cache)
     lse_ptr = None
