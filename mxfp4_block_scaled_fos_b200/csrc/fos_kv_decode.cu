@@ -338,8 +338,11 @@ __device__ __forceinline__ void make_plan(const KvAttnArgs& a, int share, int sh
 }
 
 // One row of a finished item: values d .. d + 3 and (lane 0 of the row) lse.
+// No weight, no output: o may be 0 * NaN where the cache holds one that only
+// other rows see.
 __device__ __forceinline__ void write_row(const KvAttnArgs& a, int h, int t, int hq, int d, int D, float4 o, float M,
                                           float L) {
+  if (L == 0.0f) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const float f = L == 0.0f ? 0.0f : __fdividef(a.p.vst[h], L);
   const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * f, o.y * f), y = __floats2bfloat162_rn(o.z * f, o.w * f);
   uint2 w;

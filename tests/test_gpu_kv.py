@@ -766,3 +766,19 @@ def test_overlapping_sequences_whose_rows_pass_32_bits(max_q):
     F.kv_attention(cache, q, cu, torch.zeros(batch, 1, dtype=I32, device=dev), torch.ones(batch, dtype=I32, device=dev),
                    max_q, out=out, status=status)
     assert int(status) == F.STATUS_INDEX and bool((out == 3.0).all())
+
+
+@pytest.mark.parametrize("max_q", [1, 6, 1 << 20])
+@pytest.mark.parametrize("dim,n_q,kv_len", [(128, 6, 4), (64, 6, 3), (64, 303, 41), (128, 1501, 1400)])
+def test_a_query_without_keys_is_zero_beside_a_cached_nan(dim, n_q, kv_len, max_q):
+    """NaN scales in the first token: the queries before it, in one row tile with others, still get 0 and -inf."""
+    dev = require_gpu()
+    pages, n = _paged([kv_len], 16, 160)
+    cache, _ = _random_cache(n, 16, 1, dim, 161)
+    for t in (cache.k_scales, cache.v_scales):
+        t[int(pages[0, 0]), :, 0] = 0x7F
+    out, lse = F.kv_attention(cache, _queries(n_q, 2, dim, 162).to(dev), torch.tensor([0, n_q], dtype=I32, device=dev),
+                              torch.from_numpy(pages).to(dev), torch.tensor([kv_len], dtype=I32, device=dev), max_q,
+                              return_lse=True)
+    none = n_q - kv_len
+    assert not out[:none].any() and bool(torch.isneginf(lse[:none]).all()) and bool(out[none:].isnan().all())
