@@ -782,3 +782,117 @@ def test_a_query_without_keys_is_zero_beside_a_cached_nan(dim, n_q, kv_len, max_
                               return_lse=True)
     none = n_q - kv_len
     assert not out[:none].any() and bool(torch.isneginf(lse[:none]).all()) and bool(out[none:].isnan().all())
+
+
+# many long sequences: a CTA walks tens of tiles of one item, past every reuse of a stage and of the page ids' window
+@pytest.mark.parametrize("dim,page,heads,group,q_len,batch,longest,window,causal,gain", [
+    (64, 16, 2, 8, 1, 128, 9000, 0, True, 2.0),        # 8 rows
+    (128, 16, 2, 4, 2, 128, 9000, 0, True, 6.0),       # 8 rows, maxima that rise late
+    (128, 64, 1, 3, 1, 200, 12000, 0, True, 2.0),      # 3 rows
+    (64, 32, 1, 16, 1, 100, 12000, 0, True, 6.0),      # 16 rows
+    (128, 16, 2, 4, 4, 60, 9000, 0, True, 2.0),        # 16 rows
+    (128, 128, 1, 8, 4, 60, 9000, 0, True, 2.0),       # 32 rows in two tiles
+    (64, 64, 2, 2, 3, 120, 9000, 7000, True, 6.0),     # a window over most of them
+    (128, 32, 1, 9, 1, 120, 9000, 0, False, 2.0),
+])
+def test_attention_of_many_tiles_a_cta(dim, page, heads, group, q_len, batch, longest, window, causal, gain):
+    dev = require_gpu()
+    rng = np.random.RandomState(170)
+    kv_len = [int(m) for m in rng.randint(longest // 2, longest, batch)]
+    kv_len[batch // 3], kv_len[1], kv_len[2] = q_len, longest, 0 if not causal else q_len
+    cache, ref = _random_cache(4096 // page, page, heads, dim, 171)
+    pages = rng.randint(0, 4096 // page, (batch, -(-longest // page))).astype(np.int32)   # shared by sequences
+    cu = np.arange(batch + 1) * q_len
+    q = _queries(batch * q_len, heads * group, dim, 172, gain)
+    status = torch.zeros(1, dtype=I32, device=dev)
+    out, lse = F.kv_attention(cache, q.to(dev), torch.from_numpy(cu.astype(np.int32)).to(dev),
+                              torch.from_numpy(pages).to(dev), torch.tensor(kv_len, dtype=I32, device=dev), q_len,
+                              causal=causal, window=window, return_lse=True, status=status)
+    assert int(status) == 0
+    out, lse = out.cpu().double().numpy(), lse.cpu().double().numpy()
+    for b in (0, 1, 2, batch // 3, batch // 2, batch - 1):
+        s = slice(int(cu[b]), int(cu[b + 1]))
+        want, wl, bound, lbound = R.attention(q[s], ref["kc"], ref["ks"], ref["vc"], ref["vs"], ref["kst"], ref["vst"],
+                                              [0, q_len], pages[b:b + 1], kv_len[b:b + 1], causal, window,
+                                              1 / math.sqrt(dim))
+        assert (np.abs(out[s] - want) <= bound).all(), (b, (np.abs(out[s] - want) - bound).max())
+        none = np.isinf(wl)
+        assert np.array_equal(np.isneginf(lse[s]), none)
+        assert (np.abs(lse[s][~none] - wl[~none]) <= lbound[~none]).all(), b
+
+
+# more tokens than the grid has CTAs for, in place; more lanes than a CTA (64 + 8 + 8 heads); rows of 16 and 32
+# bytes' alignment; half pairs that are not whole blocks apart at both head sizes
+@pytest.mark.parametrize("dim,page,rot,inter,fmt,tokens,heads,q_heads,aligned", [
+    (128, 64, 128, False, "nvfp4_46", 5001, 2, 4, 32),
+    (128, 16, 128, True, "nvfp4_46", 4003, 2, 4, 32),
+    (128, 16, 64, False, "nvfp4_46", 3001, 1, 8, 16),
+    (64, 32, 64, False, "nvfp4_6", 6007, 2, 3, 16),
+    (64, 64, 32, True, "nvfp4_46", 6001, 1, 1, 16),
+    (128, 128, 128, False, "nvfp4_46", 2003, 8, 64, 32),
+    (128, 16, 48, True, "nvfp4_46", 1501, 8, 64, 16),
+    (128, 16, 0, False, "nvfp4_46", 5003, 2, 0, 32),
+    (128, 32, 48, False, "nvfp4_46", 803, 2, 5, 16),
+    (128, 32, 16, False, "nvfp4_6", 803, 3, 4, 32),
+    (64, 32, 48, False, "nvfp4_46", 803, 2, 4, 32),
+])
+def test_append_of_many_tokens_in_place(dim, page, rot, inter, fmt, tokens, heads, q_heads, aligned):
+    dev = require_gpu()
+    g = torch.Generator().manual_seed(180 + tokens)
+    n = -(-tokens // page) + 2
+    cache = F.KVCache.empty(n, page, heads, dim, 3.3, 2.9, fmt=fmt, device=dev)
+    for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
+        t.fill_(0xA5)
+    x = torch.randn(tokens, q_heads + 2 * heads, dim, generator=g).to(torch.bfloat16)
+    pad = aligned // 2 % 16
+    xd = torch.zeros(tokens, x.shape[1] * dim + pad, dtype=torch.bfloat16, device=dev)[:, pad:].unflatten(1, x.shape[1:])
+    xd.copy_(x)
+    assert all(xd.data_ptr() % a == 0 for a in (16, aligned)) and (xd.stride(0) % 16 == 0) == (aligned == 32)
+    slots = torch.randperm(n * page, generator=g)[:tokens].to(torch.int64)
+    slots[3::7] = -1
+    status = torch.zeros(1, dtype=I32, device=dev)
+    want, kw = x.clone(), {}
+    if rot:
+        pos, table = torch.randint(0, 777, (tokens,), generator=g).to(I32), _table(777, rot)
+        want[:, :q_heads + heads] = R.rotate(x[:, :q_heads + heads], pos, table, inter)
+        kw = dict(positions=pos.to(dev), cos_sin=table.to(dev), interleaved=inter, q=xd[:, :q_heads],
+                  q_out=xd[:, :q_heads])
+    F.kv_append(cache, xd[:, q_heads:q_heads + heads], xd[:, q_heads + heads:], slots.to(dev), status=status, **kw)
+    assert int(status) == 0
+    assert torch.equal(xd[:, :q_heads].cpu().view(torch.int16), want[:, :q_heads].view(torch.int16))
+    assert torch.equal(xd[:, q_heads:].cpu().view(torch.int16), x[:, q_heads:].view(torch.int16))
+    live = slots >= 0
+    for y, amax, codes, scales in ((want[:, q_heads:q_heads + heads], 3.3, cache.k_codes, cache.k_scales),
+                                   (want[:, q_heads + heads:], 2.9, cache.v_codes, cache.v_scales)):
+        c, s = R.quantize(y, np.full(heads, amax, np.float32), fmt == "nvfp4_6")
+        for mine, theirs in ((codes, c), (scales, s)):
+            rows = np.full((n * page, heads, theirs.shape[-1]), 0xA5, np.uint8)
+            rows[slots[live].numpy()] = theirs[live.numpy()]
+            assert np.array_equal(mine.transpose(1, 2).reshape(n * page, heads, -1).cpu().numpy(), rows)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("each,lens", [(1, [700, 33, 0]), (3, [700, 33, 5]), (90, [700, 33, 95]), (90, [3000, 5, 95])])
+def test_strided_queries_and_outputs_and_a_callers_workspace(each, lens, dim):
+    """Queries out of a wider projection, outputs into a wider buffer, a
+    workspace that is larger than asked for and full of NaN: the same bits as
+    with dense tensors, and nothing else written."""
+    dev = require_gpu()
+    B, H, HQ = 3, 2, 6
+    pages, n = _paged(lens, 16, 190)
+    cache, _ = _random_cache(n, 16, H, dim, 191)
+    q = _queries(B * each, HQ, dim, 192).to(dev)
+    args = (torch.arange(B + 1, dtype=I32, device=dev) * each, torch.from_numpy(pages).to(dev),
+            torch.tensor(lens, dtype=I32, device=dev), each)
+    want, wl = F.kv_attention(cache, q, *args, return_lse=True)
+    wide = torch.full((B * each, (HQ + 5) * dim), 5.0, dtype=torch.bfloat16, device=dev)
+    wide[:, 8:8 + HQ * dim] = q.flatten(1)
+    out = torch.full((B * each + 2, (HQ + 1) * dim + 24), 3.0, dtype=torch.bfloat16, device=dev)
+    mine = out[1:-1, 16:16 + HQ * dim].unflatten(1, (HQ, dim))
+    size = F.kv_attention_workspace_size(cache, B * each, B, HQ, each, pages.shape[1])
+    ws = torch.full((size // 4 + 64,), math.nan, device=dev)
+    got, gl = F.kv_attention(cache, wide[:, 8:8 + HQ * dim].unflatten(1, (HQ, dim)), *args, out=mine, return_lse=True,
+                             workspace=ws)
+    assert got is mine and torch.equal(mine, want) and torch.equal(gl, wl)
+    mine.fill_(3.0)
+    assert bool((out == 3.0).all()) and bool(ws[size // 4:].isnan().all())
