@@ -78,6 +78,10 @@ int fosck_codes_at(const uint32_t* idx, long long n, int e4m3, uint32_t* out, vo
  * mismatching f16x2 results. */
 int fosck_e2m1_decode_words(const uint16_t* table16, unsigned long long* counts, void* stream);
 
+/* The same for the decoder of the key/value cache's kernels, which converts
+ * the bytes of a word as they lie in it. */
+int fosck_e2m1_decode_words_split(const uint16_t* table16, unsigned long long* counts, void* stream);
+
 /* out256[c] = binary32 value the kernels decode E4M3 code c to. */
 int fosck_e4m3_decode_all(float* out256, void* stream);
 

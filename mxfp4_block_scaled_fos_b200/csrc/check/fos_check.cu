@@ -17,8 +17,8 @@
 //    of the code over the binary32 patterns is returned for a host-side
 //    comparison (a piecewise-constant, monotone function is fixed by its
 //    transitions);
-//  * the E2M1 nibble decoder of eight packed codes, against a 16-entry table
-//    given by the host;
+//  * the E2M1 nibble decoders of eight packed codes (the quantizer's and the
+//    key/value cache's), against a 16-entry table given by the host;
 //  * the packed bf16 magnitude maximum, against the integer maximum of the
 //    magnitude bits.
 // Every kernel reads only its arguments and writes only its count words and
@@ -29,6 +29,7 @@
 
 #include "fos_check.h"
 #include "fos_core.cuh"
+#include "fos_kv.cuh"
 
 namespace {
 
@@ -254,6 +255,7 @@ __global__ void k_codes_at(const uint32_t* idx, long long n, int e4m3, uint32_t*
 // ------------------------------------------------------------ decoders
 // Every 32-bit word of eight E2M1 codes through e2m1x8_to_h2 vs the table
 // (f16 bits of each nibble's value, from the host).
+template <bool SPLIT>
 __global__ void k_e2m1_decode_words(const uint16_t* table16, unsigned long long* counts) {
   __shared__ uint16_t t[16];
   if (threadIdx.x < 16) t[threadIdx.x] = table16[threadIdx.x];
@@ -263,7 +265,8 @@ __global__ void k_e2m1_decode_words(const uint16_t* table16, unsigned long long*
        u += (unsigned long long)gridDim.x * blockDim.x) {
     const uint32_t w = (uint32_t)u;
     uint32_t h[4];
-    e2m1x8_to_h2(w, h);
+    if (SPLIT) codes_h2x4(w, h);
+    else       e2m1x8_to_h2(w, h);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t want = (uint32_t)t[(w >> (8 * k)) & 0xfu] | ((uint32_t)t[(w >> (8 * k + 4)) & 0xfu] << 16);
@@ -346,7 +349,12 @@ int fosck_codes_at(const uint32_t* idx, long long n, int e4m3, uint32_t* out, vo
 }
 
 int fosck_e2m1_decode_words(const uint16_t* table16, unsigned long long* counts, void* stream) {
-  k_e2m1_decode_words<<<kGrid, kThreads, 0, (cudaStream_t)stream>>>(table16, counts);
+  k_e2m1_decode_words<false><<<kGrid, kThreads, 0, (cudaStream_t)stream>>>(table16, counts);
+  return launched(cudaSuccess);
+}
+
+int fosck_e2m1_decode_words_split(const uint16_t* table16, unsigned long long* counts, void* stream) {
+  k_e2m1_decode_words<true><<<kGrid, kThreads, 0, (cudaStream_t)stream>>>(table16, counts);
   return launched(cudaSuccess);
 }
 

@@ -111,9 +111,10 @@ __device__ __forceinline__ uint32_t e2m1x8(float e0, float e1, float e2, float e
 }
 
 // Two E2M1 nibbles -> f16x2 (low nibble in the low half), exact.  `byte`
-// must be zero-extended (bits 8..31 clear): the conversion was measured to
-// give wrong results when the upper bits of its operand register are not
-// zero (bytes taken from a split 32-bit or 16-bit register).
+// is zero-extended (bits 8..31 clear): converted out of a split register, with
+// other bits above it, bytes gave wrong results where this was first written.
+// codes_h2x4 (fos_kv.cuh) does convert them so, and is right for all 2^32 words
+// as the library is compiled now (tests/test_gpu_exhaustive.py).
 __device__ __forceinline__ uint32_t e2m1x2_to_h2(uint32_t byte) {
   uint32_t out;
   const unsigned short t = (unsigned short)byte;

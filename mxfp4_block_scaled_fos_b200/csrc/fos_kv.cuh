@@ -32,9 +32,11 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 }
 
 // The 8 codes of a word -> four f16x2 (value 2j in the low half of h[j]).
-// Split in one move, each conversion takes its byte out of the word by
-// itself; with a byte permute for each (e2m1x2_to_h2) 47 codes a cycle and SM
-// against 72.  tests/test_gpu_kv.py compares every byte in every place.
+// The word is split in one move and its bytes converted as they are: 72 codes a
+// cycle and SM, 47 with a byte permute for each (e2m1x8_to_h2).  That one keeps
+// bytes zero-extended because split ones were once measured wrong; these are
+// compared for every word (tests/test_gpu_exhaustive.py) and, in the kernels,
+// for every byte in every place (tests/test_gpu_kv.py).
 __device__ __forceinline__ void codes_h2x4(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "mov.b32 {a, b, c, d}, %4;\n\t"
@@ -78,7 +80,8 @@ __device__ __forceinline__ bool lengths_of(const KvAttnArgs& a, int b, int& q0, 
 }
 
 // The scaling of a query row to below 2^15 by a power of two, for its f16
-// operand: exact for values down to 2^-39 of the row's largest.  up1 * up2
+// operand: exact for values down to 2^-31 of the row's largest, smaller ones
+// off by 2^-39 of it at most (half of f16's last subnormal bit).  up1 * up2
 // scales the values, down1 * down2 the scores (two factors, so that none
 // leaves the normal range); a row with NaN or Inf is not finite.
 struct RowScale {

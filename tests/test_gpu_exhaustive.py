@@ -225,3 +225,15 @@ def test_packed_bf16_magnitude_max_every_pair():
     c = _counts(1)
     _run("fosck_hmax_abs", _p(c))
     assert c.item() == 0, "%d bf16 pairs give a wrong magnitude maximum" % c.item()
+
+
+def test_cache_e2m1_decoder_every_word():
+    """codes_h2x4 of the key/value cache: bytes converted out of a split word, whatever lies beside them."""
+    dev = require_gpu()
+    vals = np.array([oracle.e2m1_decode(c) for c in range(16)], np.float32)
+    table = torch.from_numpy(vals.astype(np.float16).view(np.int16).copy()).to(dev)
+    fn = _lib().fosck_e2m1_decode_words_split
+    fn.restype, fn.argtypes = ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+    c = _counts(1)
+    _run("fosck_e2m1_decode_words_split", _p(table), _p(c))
+    assert c.item() == 0, "%d decoded words differ" % c.item()
