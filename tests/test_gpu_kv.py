@@ -896,3 +896,27 @@ def test_strided_queries_and_outputs_and_a_callers_workspace(each, lens, dim):
     assert got is mine and torch.equal(mine, want) and torch.equal(gl, wl)
     mine.fill_(3.0)
     assert bool((out == 3.0).all()) and bool(ws[size // 4:].isnan().all())
+
+
+@pytest.mark.parametrize("max_q", [None, 1, 1 << 20])
+def test_a_mixed_batch_in_one_call_or_two(max_q):
+    """A prompt beside single tokens and drafts: one call, and two over parts of
+    cu_q into the same outputs, each within the bound."""
+    dev = require_gpu()
+    q_len, kv_len = [150, 1, 3, 1, 0, 1], [210, 800, 33, 1, 5, 0]
+    pages, n = _paged(kv_len, 32, 200)
+    cache, ref = _random_cache(n, 32, 2, 128, 201)
+    cu = [0] + np.cumsum(q_len).tolist()
+    q = _queries(cu[-1], 6, 128, 202, 2.0)
+    want, _ = _check(cache, ref, q, cu, pages, kv_len, max_q=max_q)
+    qd, cd, pd = q.to(dev), torch.tensor(cu, dtype=I32, device=dev), torch.from_numpy(pages).to(dev)
+    ld = torch.tensor(kv_len, dtype=I32, device=dev)
+    out, lse = torch.empty_like(qd), torch.empty(cu[-1], 6, device=dev)
+    F.kv_attention(cache, qd, cd[:2], pd[:1], ld[:1], 150, out=out, lse=lse)
+    F.kv_attention(cache, qd, cd[1:], pd[1:], ld[1:], 3, out=out, lse=lse)
+    exact, el, bound, lbound = R.attention(q, ref["kc"], ref["ks"], ref["vc"], ref["vs"], ref["kst"], ref["vst"], cu,
+                                           pages, kv_len, True, 0, 1 / math.sqrt(128))
+    assert (np.abs(out.cpu().double().numpy() - exact) <= bound).all()
+    none = np.isinf(el)
+    got = lse.cpu().double().numpy()
+    assert np.array_equal(np.isneginf(got), none) and (np.abs(got[~none] - el[~none]) <= lbound[~none]).all()
