@@ -415,7 +415,12 @@ fos_status fos_kv_read(const fos_kv_cache* cache, const int64_t* slots, int64_t 
  *   kv_len  int32 [batch]: tokens of each sequence in the cache, those of its
  *           queries among them when causal.
  *   max_q   the largest number of queries of a sequence (it chooses between
- *           kernels; any value gives the same result up to rounding).
+ *           kernels; any value gives the same result up to rounding).  It is one
+ *           choice for all sequences: beside a long prompt, single tokens over
+ *           long contexts are slow (2048 queries and 63 single tokens over 8192
+ *           keys each, 32 heads over 8 of 128: 547 us; the tokens by themselves
+ *           147, the prompt 63).  Two calls, with cu_q, pages and kv_len from
+ *           another sequence on and the same q, out and lse, answer both.
  *   causal  query i of n sees the keys j <= kv_len - n + i, and with window
  *           > 0 only j > kv_len - n + i - window; otherwise all kv_len keys
  *           (window must be 0), as over an encoder's states.
@@ -430,10 +435,10 @@ fos_status fos_kv_read(const fos_kv_cache* cache, const int64_t* slots, int64_t 
  * stay as they were.
  *   workspace: fos_kv_attention_workspace_size(...) bytes, 16-byte aligned,
  *           not initialised, not shared by calls that overlap on the GPU.
- * Arithmetic: a query is held to 2^-23 of its largest |value| or better, its
+ * Arithmetic: a query's values are held to 2^-23 of its largest or better, its
  * products with cached keys are exact, sums are binary32, the softmax weights
  * are rounded to f16 before the second product.  A key whose score is below
- * -6e29 weighs nothing.  A cached NaN scale (kv_append writes none without
+ * -6e29 may weigh nothing.  A cached NaN scale (kv_append writes none without
  * FOS_STATUS_NONFINITE) at a position that one query of a sequence sees may
  * reach the sequence's other queries; elsewhere the cache may hold anything.
  * The work is split by the lengths alone: the same call gives the same bits.

@@ -89,9 +89,10 @@ __device__ __forceinline__ void load32(const uint16_t* p, uint4 (&w)[2]) {
 // same rows (every gridDim.y-th) of token after token and loads the next
 // token's while it works on one.
 // Memory-bound for long prompts, where the queries are most of the bytes:
-// 16384 tokens of 32 + 8 + 8 heads of 128 appended (363 MB) 75 us, 0.75 of
-// the copy bandwidth; 95 with a token for each CTA (8192 of 64 + 8 + 8 heads 73
-// and 77, 16384 of 8 + 8 + 8 heads of 64 46 and 42); one block a thread, whose
+// 16384 tokens of 32 + 8 + 8 heads of 128 appended (363 MB) 75 us in calls that
+// follow one another, 0.75 of the copy bandwidth, and 80 with nothing in L2 (86
+// with interleaved pairs); 95 with a token for each CTA (8192 of 64 + 8 + 8 heads
+// 73 and 77, 16384 of 8 + 8 + 8 heads of 64 46 and 42); one block a thread, whose
 // partners are loaded again, took 35 more.  Launch and latency for a decoding
 // step.
 // WIDE: all rows 32-byte aligned, one load and one store a block.
@@ -191,6 +192,10 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const KvAppendArgs a) {
 // not a multiple of 32): a thread has one block, and the other value of each
 // pair, rot/2 further on or back, is loaded again from a row that it shares
 // with its lanes of the warp; 8 values at a time (rot/2 is a multiple of 8).
+// A CTA for each token and no loads ahead: 16384 tokens of 32 + 8 + 8 heads of
+// 128, 48 values rotated, 117 us with nothing in L2, where k_kv_append takes 86
+// for the same rotation of interleaved pairs; of 8 + 8 + 8 heads of 64, 16
+// rotated, 47 and 39.
 template <bool F46, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 6) k_kv_append_odd(const KvAppendArgs a) {
   const int nb = a.p.dim >> 4;

@@ -58,12 +58,22 @@ fos_status check_rows(const void* x, int64_t ld, int64_t heads, int64_t dim) {
 // (queries times heads of a group) but cuts the tokens as finely as it takes
 // to fill the SMs; the one for many takes 256 rows at a time, computes 128
 // whatever there are, and gives each CTA 512 tokens at least.  Measured (us,
-// few / many; head_dim 128) by sequences times heads, on each side of the rule:
-//     2, 4000 tokens: 128 rows 18 / 23, 256 rows 21 / 30; 16000: 256 rows 39 / 40
-//     8, 4000 tokens: 64 rows 20 / 21, 96 rows 25 / 22; 16000: 37 / 35, 49 / 36
-//    16, 4000 tokens: 32 rows 20 / 23, 64 rows 28 / 26; 500: 15 / 17, 16 / 17
-//    64, 4000 tokens: 32 rows 41 / 44, 48 rows 54 / 45; 500: 20 / 18, 26 / 18
-//   256, 4000 tokens: 32 rows 126 / 141, 48 rows 180 / 142; 500: 43 / 35, 59 / 36
+// few / many, captured calls with nothing in L2) by sequences times heads, on
+// each side of the rule; head_dim 128, then 64:
+//     2,  4000 tokens: 128 rows 25 / 27, 256 rows 27 / 33;  23 / 23, 25 / 27
+//     2, 16000 tokens: 128 rows 31 / 39, 256 rows 45 / 43;  29 / 33, 39 / 37
+//     8,  4000 tokens:  64 rows 25 / 25,  96 rows 31 / 27;  23 / 23, 27 / 23
+//     8, 16000 tokens:  64 rows 43 / 39,  96 rows 55 / 41;  37 / 35, 47 / 35
+//    16,  4000 tokens:  32 rows 25 / 27,  48 rows 31 / 27;  23 / 23, 27 / 23
+//    16,   500 tokens:  32 rows 20 / 23,  48 rows 20 / 23;  18 / 18, 20 / 18
+//    64,  4000 tokens:  32 rows 47 / 49,  48 rows 59 / 49;  41 / 41, 51 / 41
+//    64,   500 tokens:  32 rows 25 / 23,  48 rows 31 / 23;  23 / 18, 29 / 18
+//   256,  4000 tokens:  32 rows 129 / 143, 48 rows 180 / 143; 106 / 115, 150 / 115
+//   256,   500 tokens:  32 rows 47 / 41,  48 rows 62 / 41;  41 / 33, 53 / 33
+// Over short tables 32 rows of many sequences would do better with the kernel
+// for many, by a tenth to a quarter: the rule does not look at the lengths, which
+// only the device knows (a table's width bounds them, and is often far above them).
+// It is one choice for the call: see the note on max_q in fos.h.
 struct AttnPlan {
   bool many;
   int rows, splits;

@@ -38,10 +38,12 @@
 //
 // Measured: 64 sequences of up to 16384 tokens (598 MB of 8 heads of 128,
 // pages of 16) 148 us with k_kv_join, 0.63 of the copy bandwidth; 4 of up to
-// 131072 tokens (407 MB) 101 us, 0.62; one of 1000 tokens 11 us.  A CTA in the
-// middle of a long item reads at 0.95 of it; beginning an item costs it 5 to
-// 7 us (page ids, digits, the first scores, the warps' results joined), which
-// the other CTA of the SM covers in part, and the plan 2 us.
+// 131072 tokens (407 MB) 101 us, 0.62; one of 1000 tokens 12 us.  More than 8
+// rows cost more (launch_kv_decode): 32 sequences of up to 16384 tokens, floor 48
+// us, 90 us with 1 to 8 rows, 125 with 16, 225 with 32.  A CTA in the middle of
+// a long item reads at 0.95 of it; beginning an item costs it 5 to 7 us (page
+// ids, digits, the first scores, the warps' results joined), which the other CTA
+// of the SM covers in part, and the plan 2 us.
 #include <math_constants.h>
 
 #include "fos_kv.cuh"

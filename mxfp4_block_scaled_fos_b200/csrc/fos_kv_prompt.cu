@@ -28,8 +28,9 @@
 // maxima 370; tensor memory 330) and its products 840 of the tensor core, the
 // other tile's meanwhile; a CTA's start and end take another 10000 to 15000, a
 // fifth of one with 17 tiles.  Measured: 8192 queries of 32 heads over 8 heads
-// of 128, causal, 562 us, 0.98 PFLOP/s, 0.57 of the measured bf16 matrix rate;
-// 6 chunks of up to 1501 queries, window 2048, head_dim 64, 106 us; 8 x 448
+// of 128, causal, 562 us, 0.98 PFLOP/s, 0.57 of the measured bf16 matrix rate,
+// in calls whose inputs change (524 with the same inputs again, as in the trials
+// below); 6 chunks of up to 1501 queries, window 2048, head_dim 64, 106 us; 8 x 448
 // queries over up to 1500 tokens, 16 heads of 64, 32 us.  Slower: two threads
 // a row (875 us), a polynomial for a quarter of the exponentials (642 against
 // 631 without), the weights handed over in halves (625 against 629: no gain), 64
@@ -97,9 +98,9 @@ __device__ __forceinline__ uint32_t desc_mn(uint32_t addr, uint32_t half) {
 }
 
 // One lane of the (converged) warp, the same each time: commits cover the
-// MMAs of the thread that issues them.  A branch on elect.sync keeps the
-// operands in uniform registers: 8192 causal queries 530 us, 541 with each MMA
-// predicated on lane 0, 5 % more again from a branch on lane 0.
+// MMAs of the thread that issues them.  8192 causal queries: 530 us with a
+// branch on elect.sync, 541 with each MMA predicated on lane 0, 5 % more again
+// from a branch on lane 0.
 __device__ __forceinline__ bool elect() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -759,9 +760,12 @@ cudaError_t launch(const KvAttnArgs& a, int splits, float* part, cudaStream_t st
 
 }  // namespace
 
-// CTAs that share an item's tokens: enough to fill 148 SMs when the items do
-// not, with four tiles of tokens for each at least.  max_q bounds the items more
-// tightly than the grid does, which must hold whatever the offsets say.
+// CTAs that share an item's tokens: enough to fill 148 SMs (a B200's; workspaces
+// are sized without asking a device) when the items do not, with four tiles of
+// tokens for each at least, as the page table's width has it: where it is far
+// above the lengths, CTAs without tokens and a join come with it.  max_q bounds
+// the items more tightly than the grid does, which must hold whatever the offsets
+// say.
 int kv_prompt_splits(long long total_q, long long batch, long long group, long long heads, long long max_q,
                      long long max_kv) {
   const long long each = batch * ((max_q * group + kRows - 1) / kRows), all = item_bound(total_q, batch, group);
