@@ -430,9 +430,10 @@ fos_status fos_kv_read(const fos_kv_cache* cache, const int64_t* slots, int64_t 
  * A query that sees no key gets out = 0 and lse = -inf.  One that sees a key
  * and holds a NaN or Inf gets NaN.  A visible page outside [0, num_pages) and a
  * kv_len beyond max_pages * page_size or below 0 set FOS_STATUS_INDEX; such keys
- * count as invisible and such lengths are clamped.  A cu_q that descends or leaves
- * [0, total_q] anywhere sets it too, and then no query is answered: out and lse
- * stay as they were.
+ * count as invisible and such lengths are clamped.  A sequence whose offsets
+ * descend or leave [0, total_q] sets it too and has no queries; if the others
+ * then have more than total_q together (they overlap), none is answered, and out
+ * and lse stay as they were.
  *   workspace: fos_kv_attention_workspace_size(...) bytes, 16-byte aligned,
  *           not initialised, not shared by calls that overlap on the GPU.
  * Arithmetic: a query's values are held to 2^-23 of its largest or better, its

@@ -64,9 +64,8 @@ __device__ __forceinline__ int query_lo(const KvAttnArgs& a, int hi) {
 }
 
 // Queries and keys of sequence b, clamped to what the arguments allow (`bad`
-// if they had to be).  False if its offsets descend or leave the queries: then
-// no sequence is answered, for whatever counts rows and items over all of them
-// (in 32 bits, for grids and loops) relies on their adding up to total_q at most.
+// if they had to be).  False if its offsets descend or leave the queries: it
+// has none then.
 __device__ __forceinline__ bool lengths_of(const KvAttnArgs& a, int b, int& q0, int& n, int& len, bool& bad) {
   const int x = a.cu_q[b], y = a.cu_q[b + 1];
   const long long cap = a.max_pages << a.p.page_shift;
@@ -77,6 +76,21 @@ __device__ __forceinline__ bool lengths_of(const KvAttnArgs& a, int b, int& q0, 
   n = ordered ? y - x : 0;
   len = max(0, (int)min((long long)m, cap));
   return ordered;
+}
+
+// Whether the sequences of a batch have more queries together than there are:
+// then none is answered, for all that counts rows and items over them (in 32
+// bits, for grids and loops) relies on total_q.  Only offsets that descend
+// somewhere can do it, so the block asks only if a sequence is not in order.
+// `mine`: this thread's sequences; sums: a place for each warp.
+__device__ __forceinline__ bool too_many(const KvAttnArgs& a, long long mine, long long* sums) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = mine;
+  __syncthreads();
+  long long all = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) all += sums[w];
+  return all > a.total_q;
 }
 
 // The scaling of a query row to below 2^15 by a power of two, for its f16

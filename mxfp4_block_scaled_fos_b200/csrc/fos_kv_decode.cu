@@ -80,7 +80,7 @@ struct Cfg {
   static constexpr int kOffRow = kOffStat + 2 * kWarps * kRows * 4;      // rs, hi, lo, query, head [rows]
   static constexpr int kOffBar = kOffRow + 5 * kRows * 4;                // of a group: scores done, keys ready
   static constexpr int kOffPlan = kOffBar + 2 * 16 + 16;
-  static constexpr int kSmem = kOffPlan + 128 + kWarps * 8 + 1024;        // + alignment slack
+  static constexpr int kSmem = kOffPlan + 128 + 2 * kWarps * 8 + 1024;    // + alignment slack
   static constexpr int kPart = kRows * (D + 2);                          // floats of one partial result
   static constexpr uint32_t kTmemCols = NT == 1 ? 128 : 256;
   static constexpr uint32_t kColSFA = 2 * kCols, kColSFB = kColSFA + 16; // + 8 * group; 4 each for both digit sets
@@ -284,18 +284,20 @@ struct Plan {
 };
 
 // Every thread of the block takes part.  The item is set unless the share is
-// empty; with broken offsets all shares are.
+// empty; all are where the sequences have too many queries.  warp_sum: two
+// numbers for each warp.
 template <int ROWS>
 __device__ __forceinline__ void make_plan(const KvAttnArgs& a, int share, int shares, Plan* plan, long long* warp_sum,
                                           bool tell) {
   const int tid = threadIdx.x, per = (a.batch + kThreads - 1) / kThreads;
   const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
-  long long mine = 0;
+  long long mine = 0, asked = 0;
   bool bad = false, ordered = true, wrong;
   Item it;
-  for (int b = b0; b < b1 && ordered; ++b) {
-    ordered = load_sequence<ROWS>(a, b, it, wrong);
+  for (int b = b0; b < b1 && asked <= a.total_q; ++b) {
+    ordered &= load_sequence<ROWS>(a, b, it, wrong);
     bad |= wrong;
+    asked += it.n;
     long long tiles = 0;
     for (int rt = 0; rt < it.nrt; ++rt) tiles += span_of<ROWS>(a, it.n, it.len, rt).tiles + kOver;
     mine += tiles * a.p.heads;
@@ -308,7 +310,7 @@ __device__ __forceinline__ void make_plan(const KvAttnArgs& a, int share, int sh
     if ((tid & 31) >= o) upto += x;
   }
   if ((tid & 31) == 31) warp_sum[tid >> 5] = upto;
-  const bool broken = __syncthreads_or(!ordered);
+  const bool broken = __syncthreads_or(!ordered) && too_many(a, asked, warp_sum + kWarps);
   long long before = 0, total = 0;
   for (int w = 0; w < kWarps; ++w) {
     if (w < (tid >> 5)) before += warp_sum[w];
@@ -871,7 +873,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_join(const KvAttnArgs a, const 
   using C = Cfg<D, NT>;
   constexpr int R = C::kRows;
   __shared__ Plan plan;
-  __shared__ long long sums[kWarps];
+  __shared__ long long sums[2 * kWarps];
   __shared__ float4 s_o[kWarps][D / 4];
   __shared__ float2 s_ml[kWarps];
   make_plan<R>(a, blockIdx.x, gridDim.x, &plan, sums, false);

@@ -59,7 +59,7 @@ struct Cfg {
   static constexpr int kOffBar = kOffScale + kRows * 4;
   static constexpr int kBars = 16;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;        // tensor memory base, failure flag, the item
-  static constexpr int kSmem = kOffMisc + 256 + 1024;         // + alignment slack
+  static constexpr int kSmem = kOffMisc + 384 + 1024;         // + alignment slack
   // kind::f16, f32 accumulator, f16 operands; M = 128
   static constexpr uint32_t kIdescS = (1u << 4) | ((kTileTok / 8) << 17) | ((128 / 16) << 24);
   static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((D / 8) << 17) | ((128 / 16) << 24);  // B MN-major
@@ -174,12 +174,13 @@ __device__ __forceinline__ void set_rows(const KvAttnArgs& a, Item& it, int rt) 
 
 // Item number `want` over all sequences (the last rows of a sequence, which
 // see the most, first); every thread of the block takes part and has it in
-// `it`.  False beyond the last item, and for all with broken offsets.  Up to 32 sequences: every warp by itself,
+// `it`.  False beyond the last item, and for all where the sequences have too
+// many queries.  Up to 32 sequences: every warp by itself,
 // a sequence for each lane, which saves the block two meetings of a start of
 // 13000 cycles (2000 for the item, 1100 to meet); more: the block together,
 // through shared memory, a sequence for each thread at once instead of 32 in turn.
 __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int threads, Item& it, Item* shared,
-                                          int* warp_sum, bool tell) {
+                                          int* warp_sum, long long* block_sum, bool tell) {
   const int tid = threadIdx.x, lane = tid & 31;
   bool bad = false, ordered = true, wrong;
   if (a.batch <= 32) {
@@ -189,7 +190,10 @@ __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int thr
       bad = wrong;
       nrt = (it.n * a.group + kRows - 1) / kRows;
     }
-    if (!__all_sync(~0u, ordered)) nrt = 0;
+    if (!__all_sync(~0u, ordered)) {      // too many queries (too_many): halves of 16 bits, that the sums fit
+      const unsigned n = nrt ? it.n : 0;
+      if (((long long)__reduce_add_sync(~0u, n >> 16) << 16) + __reduce_add_sync(~0u, n & 0xffffu) > a.total_q) nrt = 0;
+    }
     if (bad && tell && tid < 32 && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
     int upto = nrt;
 #pragma unroll
@@ -209,9 +213,11 @@ __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int thr
   const int per = (a.batch + threads - 1) / threads;
   const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
   int mine = 0;
-  for (int b = b0; b < b1 && ordered; ++b) {
-    ordered = lengths_of(a, b, it.q0, it.n, it.len, wrong);
+  long long asked = 0;
+  for (int b = b0; b < b1 && asked <= a.total_q; ++b) {
+    ordered &= lengths_of(a, b, it.q0, it.n, it.len, wrong);
     bad |= wrong;
+    asked += it.n;
     mine += (it.n * a.group + kRows - 1) / kRows;
   }
   if (bad && tell && a.status) atomicOr(a.status, FOS_STATUS_INDEX);
@@ -223,7 +229,7 @@ __device__ __forceinline__ bool find_item(const KvAttnArgs& a, int want, int thr
   }
   if (lane == 31) warp_sum[tid >> 5] = upto;
   if (tid == 0) shared->b = -1;
-  const bool broken = __syncthreads_or(!ordered);
+  const bool broken = __syncthreads_or(!ordered) && too_many(a, asked, block_sum);
   for (int w = 0; w < (tid >> 5); ++w) upto += warp_sum[w];
   int at = upto - mine;
   if (want >= at && want < upto && !broken)
@@ -319,7 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvAttnArgs a, f
   }
   Item mine;
   const bool found = find_item(a, blockIdx.x / a.p.heads, kThreads, mine, item,
-                               reinterpret_cast<int*>(smem + C::kOffMisc + 128), blockIdx.x == 0 && blockIdx.y == 0);
+                               reinterpret_cast<int*>(smem + C::kOffMisc + 128),
+                               reinterpret_cast<long long*>(smem + C::kOffMisc + 256),
+                               blockIdx.x == 0 && blockIdx.y == 0);
   const int h = blockIdx.x % a.p.heads;
   const int here = found ? mine.n * a.group - mine.rt * kRows : 0;
   // The queries of a softmax warp's 32 rows, a row for D / 8 lanes at a time,
@@ -695,8 +703,9 @@ template <int D>
 __global__ void __launch_bounds__(256) k_kv_prompt_join(const KvAttnArgs a, const float* part, int splits) {
   __shared__ Item item;
   __shared__ int sums[8];
+  __shared__ long long queries[8];
   Item it;
-  const bool found = find_item(a, blockIdx.x / a.p.heads, 256, it, &item, sums, false);
+  const bool found = find_item(a, blockIdx.x / a.p.heads, 256, it, &item, sums, queries, false);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!found) return;
   const int h = blockIdx.x % a.p.heads;

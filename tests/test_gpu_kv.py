@@ -724,32 +724,41 @@ def test_calls_that_overlap_share_no_buffers(max_q):
 
 
 @pytest.mark.parametrize("max_q", [1, 1 << 20])
-@pytest.mark.parametrize("batch,at,to", [(3, 1, 7), (3, 3, 3), (32, 31, 7), (33, 17, 0), (700, 512, 3), (700, 0, -1)])
-def test_broken_offsets_answer_no_query(batch, at, to, max_q):
-    """Offsets that descend or leave the queries anywhere: a status, and outputs as they were."""
+@pytest.mark.parametrize("batch,broken", [
+    (3, {1: 7}), (3, {3: 3}), (3, {2: 0, 3: 0}),       # outside; descending; a batch padded with zeros
+    (32, {31: 7}), (32, {31: 70}), (32, {32: 5}), (33, {17: 0}), (33, {32: 5, 33: 5}),
+    (700, {512: 3}), (700, {0: -1}), (700, {512: 4000}), (700, {i: 0 for i in range(300, 701)}),
+])
+def test_offsets_that_descend_or_leave_the_queries(batch, broken, max_q):
+    """Such a sequence has no queries and the others are answered, unless they
+    overlap and have more queries than there are: then none is. A status either way."""
     dev = require_gpu()
     cache, _ = _random_cache(3, 16, 2, 64, 140)
-    cu = list(range(0, 2 * batch + 2, 2))
-    total = cu[-1]
+    good = list(range(0, 2 * batch + 2, 2))
+    total = good[-1]
     q = _queries(total, 4, 64, 141).to(dev)
     pages = torch.zeros(batch, 2, dtype=I32, device=dev)
-    lens = torch.full((batch,), 20, dtype=I32, device=dev)
+    lens = torch.full((batch,), 20, dtype=I32, device=dev)      # the same keys for every sequence
 
     def run(cu):
         status = torch.zeros(1, dtype=I32, device=dev)
         out = torch.full((total, 4, 64), 3.0, dtype=torch.bfloat16, device=dev)
         lse = torch.full((total, 4), 3.0, device=dev)
-        F.kv_attention(cache, q, torch.tensor(cu, dtype=I32, device=dev), pages, lens, max_q, out=out, lse=lse,
-                       status=status)
-        return bool((out == 3.0).any()), bool((out == 3.0).all() and (lse == 3.0).all()), int(status)
+        F.kv_attention(cache, q, torch.tensor(cu, dtype=I32, device=dev), pages, lens, max_q, causal=False, out=out,
+                       lse=lse, status=status)
+        return out, lse, int(status)
 
-    some, _, status = run(cu)
-    assert not some and status == 0
-    for value in (to, total + 1):
-        broken = list(cu)
-        broken[at] = value
-        _, untouched, status = run(broken)
-        assert untouched and status == F.STATUS_INDEX
+    want, want_lse, status = run(good)
+    assert status == 0 and not bool((want == 3.0).all(2).any())
+    cu = [broken.get(i, x) for i, x in enumerate(good)]
+    kept = [range(x, y) for x, y in zip(cu, cu[1:]) if 0 <= x <= y <= total]
+    rows = torch.zeros(total, dtype=torch.bool, device=dev)
+    if sum(map(len, kept)) <= total:
+        rows[[i for r in kept for i in r]] = True
+    out, lse, status = run(cu)
+    assert status == F.STATUS_INDEX
+    assert torch.equal(out[rows], want[rows]) and torch.equal(lse[rows], want_lse[rows])
+    assert bool((out[~rows] == 3.0).all()) and bool((lse[~rows] == 3.0).all())
 
 
 @pytest.mark.parametrize("max_q", [1, 1 << 14])
