@@ -75,7 +75,8 @@ class KVCache:
     all on one device.  Each page is contiguous; the pages of the two codes
     (and of the two scales) pools are the same distance apart, so slices of a
     larger allocation work.  fmt: "nvfp4_46" or "nvfp4_6", for what is
-    appended (reading is the same)."""
+    appended (reading is the same).  The fields are fixed, since the calls pass
+    on their addresses: new scales, say, are copied into k_tensor_scale."""
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
                  k_tensor_scale: torch.Tensor, v_tensor_scale: torch.Tensor, fmt: str = "nvfp4_46"):
@@ -105,6 +106,11 @@ class KVCache:
                           k_codes.stride(0), k_scales.stride(0))
         self._ref = ctypes.byref(self._c)
         self._dev, self._fmt, self._scale = k_codes.get_device(), fos.FMT[fmt], 1.0 / math.sqrt(2 * half)
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:           # __init__ sets each once
+            raise AttributeError("the fields of a KVCache are fixed: copy into its tensors, or make another")
+        super().__setattr__(name, value)
 
     @classmethod
     def empty(cls, pages: int, page_size: int, heads: int, head_dim: int, k_amax: Union[float, torch.Tensor],

@@ -929,3 +929,18 @@ def test_a_mixed_batch_in_one_call_or_two(max_q):
     none = np.isinf(el)
     got = lse.cpu().double().numpy()
     assert np.array_equal(np.isneginf(got), none) and (np.abs(got[~none] - el[~none]) <= lbound[~none]).all()
+
+
+def test_new_scales_are_copied_into_a_cache():
+    dev = require_gpu()
+    cache = F.KVCache.empty(1, 16, 2, 64, 1.0, 1.0, device=dev)
+    with pytest.raises(AttributeError):
+        cache.k_tensor_scale = torch.ones(2, device=dev)
+    g = torch.Generator().manual_seed(210)
+    x = (3 * torch.randn(16, 2, 64, generator=g)).to(torch.bfloat16)
+    amax = np.array([11.0, 13.0], np.float32)
+    cache.k_tensor_scale.copy_(torch.from_numpy(amax) / 1792.0)
+    F.kv_append(cache, x.to(dev), x.to(dev), torch.arange(16, device=dev))
+    codes, scales = R.quantize(x, amax, False)
+    assert np.array_equal(cache.k_codes[0].transpose(0, 1).cpu().numpy(), codes)
+    assert np.array_equal(cache.k_scales[0].transpose(0, 1).cpu().numpy(), scales)

@@ -176,3 +176,14 @@ def test_tables_whose_tokens_pass_32_bits_are_refused(L, page_size):
 def test_a_table_width_whose_product_wraps_is_refused(L):
     for pages in (1 << 60, (1 << 60) + 1, (1 << 63) - 1):
         assert _attention(L, max_pages=pages) == SHAPE
+
+
+def test_the_fields_of_a_cache_are_fixed():
+    """A tensor or format put in a field's place would not be the one that calls use."""
+    c = object.__new__(F.KVCache)
+    c.__dict__.update(k_tensor_scale=torch.ones(1), fmt="nvfp4_46", page_size=16)
+    for name, value in (("k_tensor_scale", torch.zeros(1)), ("fmt", "nvfp4_6"), ("page_size", 32)):
+        with pytest.raises(AttributeError):
+            setattr(c, name, value)
+    c.layer = 3                           # what is no field is the user's
+    assert c.fmt == "nvfp4_46" and bool(c.k_tensor_scale == 1) and c.layer == 3
