@@ -28,9 +28,9 @@
 // maxima 370; tensor memory 330) and its products 840 of the tensor core, the
 // other tile's meanwhile; a CTA's start and end take another 10000 to 15000, a
 // fifth of one with 17 tiles.  Measured: 8192 queries of 32 heads over 8 heads
-// of 128, causal, 562 us, 0.98 PFLOP/s, 0.57 of the measured bf16 matrix rate,
-// in calls whose inputs change (524 with the same inputs again, as in the trials
-// below); 6 chunks of up to 1501 queries, window 2048, head_dim 64, 106 us; 8 x 448
+// of 128, causal, 562 to 573 us by the machine, 0.98 PFLOP/s, 0.57 of the measured
+// bf16 matrix rate, in calls whose inputs change (524 with the same inputs again, as in the
+// trials below); 6 chunks of up to 1501 queries, window 2048, head_dim 64, 106 us; 8 x 448
 // queries over up to 1500 tokens, 16 heads of 64, 32 us.  Slower: two threads
 // a row (875 us), a polynomial for a quarter of the exponentials (642 against
 // 631 without), the weights handed over in halves (625 against 629: no gain), 64
